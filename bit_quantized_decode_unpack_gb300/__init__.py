@@ -23,6 +23,7 @@ FMT_T5 = 3
 FORMATS = {"affine1": FMT_AFFINE1, "affine2": FMT_AFFINE2, "t5": FMT_T5}
 DTYPE_F16 = 1
 DTYPE_F32 = 2
+DTYPE_BF16 = 3
 
 BQD_OK = 0
 OPT_KERNEL, OPT_T5_STAGES, OPT_WAIT_LIMIT_NS, OPT_DEBUG_PLAN = 1, 2, 3, 4
@@ -81,6 +82,7 @@ def load() -> ctypes.CDLL:
         lib.bqd_set_option.restype = i32
         lib.bqd_get_option.argtypes = [i32]
         lib.bqd_get_option.restype = i64
+        kv_cache.declare(lib)
         if lib.bqd_abi_version() != ABI_VERSION:
             raise RuntimeError(f"libbqd ABI {lib.bqd_abi_version()} != binding ABI {ABI_VERSION}")
         _lib = lib
@@ -337,3 +339,8 @@ def device_status(stream=None) -> int:
     """Synchronise the stream; BQD_OK, or the status of an expired bounded
     device-side wait since the previous call (see include/bqd.h)."""
     return int(load().bqd_device_status(_stream(stream)))
+
+
+from . import kv_cache  # noqa: E402
+from .kv_cache import (KVCache, kv_append, kv_attend, kv_compact, kv_copy_pages, kv_fork,  # noqa: E402,F401
+                       kv_reserve)

@@ -1,0 +1,469 @@
+// Attention over a paged 8-bit cache for few queries of a sequence (a decode
+// step, the verification of draft tokens).
+//
+// With c^k, c^v the codes, s^k_b, s^v_b the scales of block b (16 tokens) and
+// f = scale log2(e), all in powers of two:
+//   x_j = f s^k_b (q . c^k_j) + log2 s^v_b          (j in block b; masked: -inf)
+//   p_j = 2^(x_j - m),  m >= max x - 8 per query, grown when a tile passes it
+//   O = sum_j p_j c^v_j,   l = sum_b (sum_{j in b} p_j) / s^v_b
+//   out = O / l,   lse = ln 2 (m + log2 l)
+// Both scales cost nothing per value: K's is folded into the fma that forms
+// x, V's into its addend, and l takes one product a block.  p includes V's
+// scale, so the fp16 rounding of p is relative to the largest contribution to
+// O whatever the spread of the scales; l adds the fp32 values before it.
+//
+// Layout.  A warp takes 16-token tiles: S = K q^T and O^T = V^T p run as
+// mma.sync m16n8k16 with the cache as the 16-row operand, because a group of
+// q_heads / kv_heads queries fills 8 columns far better than 16 rows.  The
+// contraction index may be permuted freely, so a lane's A fragment of K is 16
+// contiguous bytes a chunk of its token row, and of V 16 contiguous bytes of
+// each of its four tokens: both operands go from global memory to registers by
+// fully used 16-byte loads, and a byte permute that converts to fp16 also
+// interleaves two tokens' bytes for V.  K's registers are refilled for the
+// next tile as soon as the scores are done, V's after the second product, so
+// a tile (32 D bytes) is always in flight for each warp.
+// Codes are exact in fp16 and q is scaled by a power of two into its range.
+//
+// The keys of one (row, KV head, column tile) are split over the 8 warps of a
+// CTA and the S CTAs of a cluster; partial (m, l, O) are joined through shared
+// and distributed shared memory in a fixed order: one launch, no scratch, the
+// same bits every time.
+#include <algorithm>
+#include <cmath>
+
+#include "kv_common.cuh"
+#include "qmv_common.cuh"
+
+namespace bqd {
+namespace kv {
+namespace {
+
+using namespace qmvdev;
+
+constexpr int kWarpsD = 8;
+constexpr int kMaxSplit = 16;  // CTAs of a cluster
+constexpr float kGrow = 8.0f;  // a reference m is replaced when x passes it by this much
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x)
+{
+    uint32_t d;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+    return d;
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t local_addr, uint32_t rank)
+{
+    uint32_t remote;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(remote) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t local_addr, uint32_t rank)
+{
+    uint32_t remote;
+    float4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(remote) : "r"(local_addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(remote)
+                 : "memory");
+    return v;
+}
+
+template <int D, int NT>
+struct Tile {
+    static constexpr int kCols = 8 * NT;
+    static constexpr int kPitch = D + 4;  // floats of a column in shared memory
+    // floats: per-warp partials, then the CTA's joined partial and its m, l
+    static constexpr int kWarpFloats = kCols * kPitch;
+    static constexpr size_t kSmem = sizeof(float) * ((size_t)kWarpsD * kWarpFloats + 2 * kWarpsD * kCols +
+                                                     (size_t)kWarpFloats + 2 * kCols);
+};
+
+template <typename T, int D, int FMT, int NT>
+__global__ void __launch_bounds__(kWarpsD * 32, (D == 256 || NT > 1) ? 1 : 2)
+attend_decode_kernel(const AttendArgs a, int S)
+{
+    using C = Code<FMT>;
+    using H = Half2Of<T>;
+    using TL = Tile<D, NT>;
+    constexpr int KW = D / 16;   // 32-bit words of a lane's part of one K row
+    constexpr int VW = D / 32;   // words of a lane's part of one V token
+    constexpr int KS = D / 16;   // k16 steps of S, m16 tiles of O^T
+    extern __shared__ __align__(16) float smem[];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, t = lane & 3;
+    const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+    const int ctile = blockIdx.x / S, head = blockIdx.y, row = blockIdx.z;
+    const Span span(a.starts, row, a.tokens, a.max_new);
+    const int cols = span.n * a.group;       // columns: query-major, then head of the group
+    const int c0 = ctile * TL::kCols;
+    if (c0 >= cols) return;                  // the whole cluster leaves
+    const int L = a.L.length(row);
+    const int i_min = c0 / a.group, i_max = (min(c0 + TL::kCols, cols) - 1) / a.group;
+    const int p_min = L - span.n + i_min, p_max = L - span.n + i_max;
+    const int hi = max(0, p_max + 1);
+    const int lo = a.window > 0 ? max(0, p_min + 1 - a.window) : 0;
+    // this CTA's tiles [j0, j1) of 16 tokens
+    const int tile_lo = lo >> 4, tiles = max(0, ((hi + 15) >> 4) - tile_lo);
+    const int j0 = tile_lo + (int)((int64_t)tiles * rank / S), j1 = tile_lo + (int)((int64_t)tiles * (rank + 1) / S);
+
+    // q: column n*8 + g, the dims of this lane's K chunks, scaled by 2^-e
+    uint32_t qf[NT][KS][2];
+    float cs[NT][2];             // f 2^e of columns n*8 + 2t, + 2t + 1
+    int pos[NT][2];              // their positions (-1: nothing)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int c = c0 + n * 8 + g;
+        uint32_t w[2 * KW];
+        if (c < cols) {
+            const T *q = static_cast<const T *>(a.q) + (int64_t)(span.lo + c / a.group) * a.q_token +
+                         (int64_t)(head * a.group + c % a.group) * a.q_head;
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const T *at = q + 16 * (t + 4 * j);
+                if (a.q_vec) {
+                    const uint4 v0 = __ldg(reinterpret_cast<const uint4 *>(at));
+                    const uint4 v1 = __ldg(reinterpret_cast<const uint4 *>(at) + 1);
+                    w[8 * j] = v0.x, w[8 * j + 1] = v0.y, w[8 * j + 2] = v0.z, w[8 * j + 3] = v0.w;
+                    w[8 * j + 4] = v1.x, w[8 * j + 5] = v1.y, w[8 * j + 6] = v1.z, w[8 * j + 7] = v1.w;
+                } else {
+                    const unsigned short *u = reinterpret_cast<const unsigned short *>(at);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        w[8 * j + e] = (uint32_t)__ldg(u + 2 * e) | ((uint32_t)__ldg(u + 2 * e + 1) << 16);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 2 * KW; ++e) w[e] = 0;
+        }
+        uint32_t mx = 0;
+#pragma unroll
+        for (int e = 0; e < 2 * KW; ++e) mx = __vmaxu2(mx, w[e] & 0x7FFF7FFFu);
+        uint32_t top = max(mx & 0xFFFFu, mx >> 16);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // exponent of the largest |q|; 0 for an all-zero row and for infinities and NaN
+        int e = 0;
+        if (top != 0 && top < H::kInf) e = max(-100, min(126, (int)((__float_as_uint(H::f1(top)) >> 23) & 0xFF) - 127));
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float2 f = H::f2(w[2 * k + h]);
+                qf[n][k][h] = Half2Of<__half>::pack(f.x * down, f.y * down);
+            }
+        const float mine = a.scale * up;
+        cs[n][0] = __shfl_sync(0xffffffffu, mine, 8 * t);
+        cs[n][1] = __shfl_sync(0xffffffffu, mine, 8 * t + 4);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int cc = c0 + n * 8 + 2 * t + h;
+            pos[n][h] = cc < cols ? L - span.n + cc / a.group : -1;
+        }
+    }
+
+    float acc[NT][KS][4];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) acc[n][k][0] = acc[n][k][1] = acc[n][k][2] = acc[n][k][3] = 0.0f;
+    }
+
+    uint32_t kw[2][KW], vw[4][VW];
+    float ksc = 0.0f, vsc = 1.0f;
+    auto load_k = [&](int64_t blk) {
+        const uint8_t *at = a.L.k + blk * (kBlock * D) + 16 * t;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const uint4 v = ld_stream_v4(at + (g + 8 * r) * D + 64 * j);
+                kw[r][4 * j] = v.x, kw[r][4 * j + 1] = v.y, kw[r][4 * j + 2] = v.z, kw[r][4 * j + 3] = v.w;
+            }
+        ksc = __ldg(a.L.ks + blk);
+    };
+    auto load_v = [&](int64_t blk) {
+        const uint8_t *at = a.L.v + blk * (kBlock * D);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint8_t *tok = at + (2 * t + (r & 1) + 8 * (r >> 1)) * D;
+            if constexpr (D == 64) {
+                const uint2 v = ld_stream_v2(tok + 8 * g);
+                vw[r][0] = v.x, vw[r][1] = v.y;
+            } else {
+#pragma unroll
+                for (int j = 0; j < D / 128; ++j) {
+                    const uint4 v = ld_stream_v4(tok + 16 * (g + 8 * j));
+                    vw[r][4 * j] = v.x, vw[r][4 * j + 1] = v.y, vw[r][4 * j + 2] = v.z, vw[r][4 * j + 3] = v.w;
+                }
+            }
+        }
+        vsc = __ldg(a.L.vs + blk);
+    };
+
+    int j = j0 + warp;
+    int64_t blk = 0;
+    int next_page = 0;  // as listed, of the tile after the next
+    if (j < j1) {
+        blk = a.L.block_of(row, head, j << 4);
+        load_k(blk);
+        load_v(blk);
+        if (j + kWarpsD < j1) next_page = a.L.listed(row, (j + kWarpsD) << 4);
+    }
+    for (; j < j1; j += kWarpsD) {
+        const int t0 = j << 4;
+        const bool more = j + kWarpsD < j1;
+        int64_t next = 0;
+        if (more) {
+            next = a.L.block_at((unsigned)next_page < (unsigned)a.L.pages ? next_page : 0, head, (j + kWarpsD) << 4);
+            if (j + 2 * kWarpsD < j1) next_page = a.L.listed(row, (j + 2 * kWarpsD) << 4);
+        }
+        // scores of 16 tokens
+        float s[NT][4];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+            const uint32_t u0 = C::ready(kw[0][k]), u1 = C::ready(kw[1][k]);
+            const uint32_t a0 = C::template pair<0>(u0), a1 = C::template pair<0>(u1);
+            const uint32_t a2 = C::template pair<1>(u0), a3 = C::template pair<1>(u1);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma16816(s[n], a0, a1, a2, a3, qf[n][k][0], qf[n][k][1]);
+        }
+        const float kscale = ksc, vscale = vsc;
+        if (more) load_k(next);
+
+        const float lv = __log2f(vscale), rv = __frcp_rn(vscale);
+        const bool whole = t0 + 15 <= p_min && (a.window == 0 || t0 > p_max - a.window);
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float f0 = cs[n][0] * kscale, f1 = cs[n][1] * kscale;
+            float x[4] = {fmaf(s[n][0], f0, lv), fmaf(s[n][1], f1, lv), fmaf(s[n][2], f0, lv), fmaf(s[n][3], f1, lv)};
+            if (!whole) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tok = t0 + g + 8 * (e >> 1), pp = pos[n][e & 1];
+                    if (tok > pp || (a.window > 0 && tok <= pp - a.window)) x[e] = -INFINITY;
+                }
+            }
+            const float x0 = fmaxf(x[0], x[2]), x1 = fmaxf(x[1], x[3]);
+            if (__any_sync(0xffffffffu, x0 > m[n][0] + kGrow || x1 > m[n][1] + kGrow)) {
+                float n0 = x0, n1 = x1;
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) {
+                    n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
+                    n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
+                }
+                n0 = fmaxf(n0, m[n][0]), n1 = fmaxf(n1, m[n][1]);
+                // -inf - -inf: nothing yet, nothing to scale
+                const float r0 = n0 == -INFINITY ? 1.0f : ex2(m[n][0] - n0);
+                const float r1 = n1 == -INFINITY ? 1.0f : ex2(m[n][1] - n1);
+                m[n][0] = n0, m[n][1] = n1;
+                l[n][0] *= r0, l[n][1] *= r1;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    acc[n][k][0] *= r0, acc[n][k][2] *= r0;
+                    acc[n][k][1] *= r1, acc[n][k][3] *= r1;
+                }
+            }
+            const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
+            const float e0 = ex2(x[0] - m0), e1 = ex2(x[1] - m1), e2 = ex2(x[2] - m0), e3 = ex2(x[3] - m1);
+            l[n][0] = fmaf(e0 + e2, rv, l[n][0]);
+            l[n][1] = fmaf(e1 + e3, rv, l[n][1]);
+            pb[n][0] = transpose8x8(Half2Of<__half>::pack(e0, e1));
+            pb[n][1] = transpose8x8(Half2Of<__half>::pack(e2, e3));
+        }
+        if (FMT == BQD_KV_E4M3 && t0 + 15 >= L) {
+            // bytes past the row's end may be anything, NaN among them, and 0 * NaN is NaN
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                if (t0 + 2 * t + (r & 1) + 8 * (r >> 1) >= L) {
+#pragma unroll
+                    for (int w = 0; w < VW; ++w) vw[r][w] = 0;
+                }
+        }
+        // O^T += V^T p: word w of the lane's tokens gives m tiles 2w, 2w + 1
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+            const uint32_t v0 = C::ready(vw[0][w]), v1 = C::ready(vw[1][w]);
+            const uint32_t v2 = C::ready(vw[2][w]), v3 = C::ready(vw[3][w]);
+            const uint32_t a01 = __byte_perm(v0, v1, 0x5140), b01 = __byte_perm(v0, v1, 0x7362);
+            const uint32_t a23 = __byte_perm(v2, v3, 0x5140), b23 = __byte_perm(v2, v3, 0x7362);
+            const uint32_t x0 = C::template pair<0>(a01), x1 = C::template pair<1>(a01);
+            const uint32_t x2 = C::template pair<0>(a23), x3 = C::template pair<1>(a23);
+            const uint32_t y0 = C::template pair<0>(b01), y1 = C::template pair<1>(b01);
+            const uint32_t y2 = C::template pair<0>(b23), y3 = C::template pair<1>(b23);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                mma16816(acc[n][2 * w], x0, x1, x2, x3, pb[n][0], pb[n][1]);
+                mma16816(acc[n][2 * w + 1], y0, y1, y2, y3, pb[n][0], pb[n][1]);
+            }
+        }
+        if (more) load_v(next);
+    }
+
+    // ---- join the warps --------------------------------------------------------
+    float *part = smem;                                  // [warp][col][kPitch]
+    float *wm = part + kWarpsD * TL::kWarpFloats;        // [warp][col]
+    float *wl = wm + kWarpsD * TL::kCols;
+    float *joined = wl + kWarpsD * TL::kCols;            // [col][kPitch]
+    float *jm = joined + TL::kWarpFloats, *jl = jm + TL::kCols;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            float sum = l[n][h];
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            const int col = n * 8 + 2 * t + h;
+            if (g == 0) {
+                wm[warp * TL::kCols + col] = m[n][h];
+                wl[warp * TL::kCols + col] = sum;
+            }
+            // m tile i holds dims base + 2i, + 1 (rows g and g + 8)
+            float *at = part + warp * TL::kWarpFloats + col * TL::kPitch;
+#pragma unroll
+            for (int k = 0; k < KS; k += 2) {
+                const int d = D == 64 ? 8 * g + 2 * k : 16 * (g + 8 * (k / 8)) + 2 * (k % 8);
+                *reinterpret_cast<float4 *>(at + d) =
+                    make_float4(acc[n][k][h], acc[n][k][2 + h], acc[n][k + 1][h], acc[n][k + 1][2 + h]);
+            }
+        }
+    }
+    __syncthreads();
+    auto finish = [&](int col, int d, float4 o, float mm, float ll) {
+        const int c = c0 + col;
+        if (c >= cols) return;
+        const int token = span.lo + c / a.group, hq = head * a.group + c % a.group;
+        const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
+        T *at = static_cast<T *>(a.out) + ((int64_t)token * a.q_heads + hq) * D + d;
+        *reinterpret_cast<uint2 *>(at) = make_uint2(H::pack(o.x * r, o.y * r), H::pack(o.z * r, o.w * r));
+        if (a.lse && d == 0)
+            a.lse[(int64_t)token * a.q_heads + hq] =
+                ll == 0.0f ? -INFINITY : 0.69314718055994531f * (mm + log2f(ll));
+    };
+    constexpr int kQuads = TL::kCols * D / 4;
+    for (int i = threadIdx.x; i < kQuads; i += kWarpsD * 32) {
+        const int col = i / (D / 4), d = (i % (D / 4)) * 4;
+        float mm = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarpsD; ++w) mm = fmaxf(mm, wm[w * TL::kCols + col]);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float ll = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarpsD; ++w) {
+            const float mw = wm[w * TL::kCols + col];
+            const float r = mw == -INFINITY ? 0.0f : ex2(mw - mm);
+            const float4 v = *reinterpret_cast<const float4 *>(part + w * TL::kWarpFloats + col * TL::kPitch + d);
+            o.x = fmaf(v.x, r, o.x), o.y = fmaf(v.y, r, o.y), o.z = fmaf(v.z, r, o.z), o.w = fmaf(v.w, r, o.w);
+            ll = fmaf(wl[w * TL::kCols + col], r, ll);
+        }
+        if (S == 1) {
+            finish(col, d, o, mm, ll);
+        } else {
+            *reinterpret_cast<float4 *>(joined + col * TL::kPitch + d) = o;
+            if (d == 0) jm[col] = mm, jl[col] = ll;
+        }
+    }
+    if (S == 1) return;
+    // ---- join the CTAs: rank r finishes the quads r, r + S, ... ------------------
+    cluster_sync();
+    for (int i = threadIdx.x * S + rank; i < kQuads; i += kWarpsD * 32 * S) {
+        const int col = i / (D / 4), d = (i % (D / 4)) * 4;
+        float mm = -INFINITY;
+        for (int r = 0; r < S; ++r) mm = fmaxf(mm, ld_cluster_f32(smem_addr(jm + col), r));
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float ll = 0.0f;
+        for (int r = 0; r < S; ++r) {
+            const float mr = ld_cluster_f32(smem_addr(jm + col), r);
+            const float f = mr == -INFINITY ? 0.0f : ex2(mr - mm);
+            const float4 v = ld_cluster_f32x4(smem_addr(joined + col * TL::kPitch + d), r);
+            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+            ll = fmaf(ld_cluster_f32(smem_addr(jl + col), r), f, ll);
+        }
+        finish(col, d, o, mm, ll);
+    }
+    cluster_sync();  // no CTA leaves while another reads its shared memory
+}
+
+// Makes a kernel ready on the current device, once per device.
+template <typename K>
+bool configure(K kern, size_t smem, bool (&done)[64])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev >= 0 && dev < 64 && done[dev]) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess)
+        return false;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+    return true;
+}
+
+template <typename T, int D, int FMT, int NT>
+int launch_t(const AttendArgs &a, cudaStream_t s)
+{
+    auto kern = attend_decode_kernel<T, D, FMT, NT>;
+    using TL = Tile<D, NT>;
+    static bool done[64] = {};
+    if (!configure(kern, TL::kSmem, done)) return BQD_ERR_CUDA;
+    const int64_t ctiles = ((int64_t)a.max_new * a.group + TL::kCols - 1) / TL::kCols;
+    const int64_t units = ctiles * a.L.heads * a.L.rows;
+    // split the keys until there are two CTAs an SM, as long as each warp
+    // keeps two tiles
+    int S = 1;
+    while (S < kMaxSplit && units * S < 2 * sm_count() && a.max_len >= 2 * kBlock * kWarpsD * 2 * S) S *= 2;
+    cudaLaunchConfig_t cfg = {};
+    if (ctiles * S > 0x7FFFFFFF) return BQD_ERR_INVALID_ARG;
+    cfg.gridDim = dim3((unsigned)(ctiles * S), (unsigned)a.L.heads, (unsigned)a.L.rows);
+    cfg.blockDim = dim3(kWarpsD * 32);
+    cfg.dynamicSmemBytes = TL::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = S;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cuda_status(cudaLaunchKernelEx(&cfg, kern, a, S));
+}
+
+template <typename T, int FMT>
+int launch_d(const AttendArgs &a, cudaStream_t s)
+{
+    if (a.head_dim == 64) return launch_t<T, 64, FMT, 1>(a, s);
+    if (a.head_dim == 128) return launch_t<T, 128, FMT, 1>(a, s);
+    return launch_t<T, 256, FMT, 1>(a, s);
+}
+
+}  // namespace
+
+int launch_attend_decode(const AttendArgs &a, cudaStream_t s)
+{
+    if (a.format == BQD_KV_INT8)
+        return a.dtype == BQD_DTYPE_F16 ? launch_d<__half, BQD_KV_INT8>(a, s)
+                                        : launch_d<__nv_bfloat16, BQD_KV_INT8>(a, s);
+    return a.dtype == BQD_DTYPE_F16 ? launch_d<__half, BQD_KV_E4M3>(a, s)
+                                    : launch_d<__nv_bfloat16, BQD_KV_E4M3>(a, s);
+}
+
+}  // namespace kv
+}  // namespace bqd

@@ -1,7 +1,8 @@
 /*
  * bqd.h -- C ABI of libbqd: the decode-time low-bit quantized matrix-vector
- * product (QMV), its prefill matrix product (QMM) and the speculative-decoding
- * verification kernel, on GB300 (sm_103a).
+ * product (QMV), its prefill matrix product (QMM), the speculative-decoding
+ * verification kernel and a paged 8-bit KV cache (append, attention over it,
+ * page operations), on GB300 (sm_103a).
  *
  * Page defining the operations: "oMLX Bonsai 自定义内核:Qwen 系列快速 QMV 路径
  * 完整解析" (oMLX Bonsai custom kernels: the fast QMV path for the Qwen
@@ -68,8 +69,15 @@ enum {
 /* weight formats */
 enum { BQD_FMT_AFFINE1 = 1, BQD_FMT_AFFINE2 = 2, BQD_FMT_T5 = 3 };
 
-/* element types of bqd_spec_decode_verify's logits */
-enum { BQD_DTYPE_F16 = 1, BQD_DTYPE_F32 = 2 };
+/* element types: F16 and F32 for bqd_spec_decode_verify's logits, F16 and BF16
+ * for the tensors of the KV cache's entry points */
+enum { BQD_DTYPE_F16 = 1, BQD_DTYPE_F32 = 2, BQD_DTYPE_BF16 = 3 };
+
+/* code types of the KV cache */
+enum { BQD_KV_INT8 = 1, BQD_KV_E4M3 = 2 };
+
+/* tokens that share one scale of the KV cache */
+#define BQD_KV_BLOCK 16
 
 /* opaque CUDA stream (binary-compatible with cudaStream_t / CUstream) */
 typedef struct CUstream_st *bqd_stream_t;
@@ -200,6 +208,152 @@ int bqd_detect_sym(const void *scales, const void *biases, int64_t N, int64_t G,
 int bqd_spec_decode_verify(const void *logits, int dtype, const int32_t *draft, int64_t B, int64_t D,
                            int64_t V, int32_t *accepted, int32_t *next_token, int32_t *argmax_out,
                            bqd_stream_t stream);
+
+/*
+ * Paged 8-bit KV cache.  The page this library follows stops at the linear
+ * layers and the verification step; the cache below is what a decode step
+ * reads and writes between the k/v projections and the o projection.
+ *
+ * A stored value is code * scale, with an 8-bit code (BQD_KV_INT8: -127..127;
+ * BQD_KV_E4M3: finite e4m3) and one fp32 scale for each block of BQD_KV_BLOCK
+ * tokens and head (K and V apart).  Rows (sequences) list their pages in
+ * `table`: token p of row r is token p % page_tokens of page
+ * table[r, p / page_tokens].  All layers share the table.  The struct holds
+ * device pointers and sizes; the caller owns everything it points to:
+ *   k_codes, v_codes    [layers, pages, kv_heads, page_tokens, head_dim], 1
+ *                       byte a code, 16-byte aligned
+ *   k_scales, v_scales  fp32 [layers, pages, kv_heads, page_tokens / 16]
+ *   table               int32 [rows, row_pages]; entries past a row's last
+ *                       page are not read (the library writes -1 there)
+ *   lens                int32 [rows]: tokens of each row (0: an empty row)
+ *   refs                int32 [pages]: table entries (and pins of the caller)
+ *                       that name the page; 0 = free
+ * head_dim is 64, 128 or 256; page_tokens 16, 32, 64, 128 or 256; rows <=
+ * 65535; row_pages * page_tokens < 2^30; pages < 2^30.  Page ids and lengths
+ * are device data and are not checked on the host: an id outside [0, pages)
+ * is read as page 0 (written: skipped) and a length is cut to the table's
+ * capacity, so that no access leaves the pools.
+ */
+typedef struct bqd_kv_cache {
+    void *k_codes, *v_codes;
+    float *k_scales, *v_scales;
+    int32_t *table;
+    int32_t *lens;
+    int32_t *refs;
+    int64_t pages;
+    int32_t layers, kv_heads, head_dim, page_tokens;
+    int32_t rows, row_pages;
+    int32_t format; /* BQD_KV_INT8 or BQD_KV_E4M3 */
+    int32_t reserved; /* 0 */
+} bqd_kv_cache;
+
+/*
+ * Quantise new keys and values into the cache of one layer.  Row r's new
+ * tokens are starts[r] .. starts[r+1]-1 of k and v (starts == NULL: token r,
+ * one for each row) and go to positions base[r], base[r]+1, ... (base[r] < 0:
+ * the row is skipped); bqd_kv_reserve gives base and the pages.
+ * A block that gets new values takes the scale
+ *     s' = max(s, fp32(max(amax, 2^-80) * fp32(1 / top))),  top = 127 or 448,
+ * amax over the finite new values of the block and head, s the block's scale
+ * if it holds tokens before base[r] and 0 otherwise.  With r = fp32(1 / s'),
+ * new codes are rnd(fp32(x * r)) and, where s' > s, the earlier tokens' codes
+ * become rnd(fp32(fp32(code * s) * r)): round to nearest even, infinities and
+ * larger values clamped to +-top, NaN stored as 0.  Appending the same tokens
+ * twice gives the same bytes as appending them once.
+ *   k, v    device [tokens, kv_heads, head_dim] of `dtype` (F16 or BF16), each
+ *           with its own strides of token and head, in elements; head_dim is
+ *           contiguous.  16-byte aligned bases with strides of multiples of 8
+ *           take 16-byte loads, others element loads
+ *   base    device int32 [rows];  starts device int32 [rows + 1] or NULL
+ *   tokens  rows of k and v (== rows when starts is NULL)
+ *   max_new an upper bound of starts[r+1] - starts[r] (later tokens of a row
+ *           are not stored)
+ * A page that two rows list must not be appended to through either
+ * (bqd_kv_reserve replaces it).  Returns BQD_OK, BQD_ERR_INVALID_ARG,
+ * BQD_ERR_ALIGNMENT or BQD_ERR_CUDA.
+ */
+int bqd_kv_append(const bqd_kv_cache *cache, int layer, const void *k, int64_t k_token_stride,
+                  int64_t k_head_stride, const void *v, int64_t v_token_stride, int64_t v_head_stride, int dtype,
+                  const int32_t *base, const int32_t *starts, int64_t tokens, int64_t max_new,
+                  bqd_stream_t stream);
+
+/*
+ * Attention over the cache of one layer.  Row r's queries are starts[r] ..
+ * starts[r+1]-1 of q (starts == NULL: query r, one for each row), n of them,
+ * at positions lens[r] - n + i: the cache already holds their own tokens.
+ * Query i sees the keys j <= p = lens[r] - n + i (and j > p - window where
+ * window > 0); head h reads KV head h / (q_heads / kv_heads):
+ *     out = sum_j softmax_j(scale * q . K_j) V_j,
+ *     lse = log sum_j exp(scale * q . K_j)   (natural logarithm)
+ * A query that sees no key (an empty row, or p < 0) gives 0 and -infinity.
+ * Scores, softmax sums and outputs accumulate in fp32; the weights that meet
+ * V are rounded to fp16 after a power-of-two scaling that keeps the largest
+ * near 1.
+ *   q       device [tokens, q_heads, head_dim] of `dtype` (F16 or BF16), strides
+ *           of token and head in elements, head_dim contiguous
+ *   out     device [tokens, q_heads, head_dim] of `dtype`, dense, 16-byte
+ *           aligned; rows of q outside every row's range are left as they are
+ *   lse     device fp32 [tokens, q_heads] or NULL
+ *   max_new an upper bound of starts[r+1] - starts[r] (later queries of a row
+ *           are not computed); max_len a bound of lens that the launch is
+ *           planned for (0: the table's capacity); longer rows stay correct
+ *   scale   finite;  window >= 0 (0: none)
+ * Returns BQD_OK, BQD_ERR_INVALID_ARG, BQD_ERR_ALIGNMENT or BQD_ERR_CUDA.
+ */
+int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride,
+                  int64_t q_head_stride, int dtype, int q_heads, const int32_t *starts, int64_t tokens,
+                  int64_t max_new, int64_t max_len, float scale, int64_t window, void *out, float *lse,
+                  bqd_stream_t stream);
+
+/*
+ * Room for counts[r] more tokens in each row (counts == NULL: one for each
+ * row that is not empty).  lens grows, table gets the new pages (free pages,
+ * lowest index first, in the order of the rows and of their tokens) and refs
+ * follows.  A partly filled last page that other table entries name too is
+ * first replaced by a copy (all layers, K, V and scales); where all its
+ * references are rows of this call that end in it, the first of them keeps it.
+ *   base    device int32 [rows]: length before the call, or -1 where the call
+ *           failed
+ *   copies  device int32 [rows, 2]: (source, copy) of a row's replaced page,
+ *           or (-1, -1)
+ *   status  device int32 [2]: pages that were missing, and rows that the table
+ *           has no room for.  (0, 0) is success; otherwise nothing changes.
+ * counts device int32 [rows], >= 0.  rows <= 4096.
+ */
+int bqd_kv_reserve(const bqd_kv_cache *cache, const int32_t *counts, int32_t *base, int32_t *copies,
+                   int32_t *status, bqd_stream_t stream);
+
+/*
+ * New rows from old ones: row i of `to` lists the pages of the first
+ * min(keep[i], lens[parents[i]]) tokens of row parents[i] of `from` (keep ==
+ * NULL: all; a parent outside [0, rows): an empty row), and to->refs = from->
+ * refs minus what from's rows name plus what to's rows name.  This forks
+ * (beams), reorders, cuts back (rejected draft tokens) and frees rows.
+ * `from` and `to` share pools and sizes but for rows; table, lens and refs of
+ * `to` are other memory than those of `from`, and every page is shared: no
+ * K or V moves.  parents, keep: device int32 [to->rows].
+ */
+int bqd_kv_fork(const bqd_kv_cache *from, const bqd_kv_cache *to, const int32_t *parents, const int32_t *keep,
+                bqd_stream_t stream);
+
+/*
+ * Compaction: with L live pages (refs > 0), the k-th live page at an index >=
+ * L moves to the k-th free index below L, in every layer; `to` gets the table,
+ * lens and refs that follow (other memory than those of `from`; pools and
+ * sizes are the same).  The bytes of a page that moved away stay as they are.
+ *   work    device int32 [2 * pages], scratch
+ *   moved   device int32 [1]: pages moved
+ */
+int bqd_kv_compact(const bqd_kv_cache *from, const bqd_kv_cache *to, int32_t *work, int32_t *moved,
+                   bqd_stream_t stream);
+
+/*
+ * Copy page src[i] to page dst[i], i < n, in every layer (K, V and scales).
+ * src and dst: device int32 [n]; no page may be in both, nor twice in dst.
+ * Ids outside [0, pages) are skipped.
+ */
+int bqd_kv_copy_pages(const bqd_kv_cache *cache, const int32_t *src, const int32_t *dst, int64_t n,
+                      bqd_stream_t stream);
 
 /*
  * Device-side failure report.  Kernels that wait on asynchronous copies

@@ -11,7 +11,8 @@ Two independent implementations of the same definitions:
 * ``oracle.py`` (NumPy, whole-matrix array operations).
 
 ``spec_verify.py`` holds the oracle of the speculative-decoding verification
-step (plain Python loops).
+step (plain Python loops), ``kv_cache.py`` that of the paged 8-bit KV cache
+(checked in ``tests/test_kv_oracle.py``).
 
 Parity pins: every function here is checked in ``tests/test_oracle_pins.py``
 against closed forms, exhaustive enumerations and brute force.  None of them
@@ -28,6 +29,7 @@ from pathlib import Path
 import numpy as np
 
 from . import oracle as np_oracle  # noqa: F401  (the NumPy twin)
+from . import kv_cache  # noqa: F401  (the paged 8-bit KV cache)
 from .spec_verify import spec_decode_verify  # noqa: F401  (speculative-decoding verification)
 from .oracle import (DEFAULT_SYM_RATIO, FMT_AFFINE1, FMT_AFFINE2, FMT_T5,  # noqa: F401
                      FORMATS, GROUP_SIZES, MAX_CODE, t5_bytes_per_group)
