@@ -259,7 +259,7 @@ extern "C" int bqd_detect_sym(const void *scales, const void *biases, int64_t N,
 extern "C" int bqd_device_status(bqd_stream_t stream)
 {
     if (cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess) return BQD_ERR_CUDA;
-    unsigned int n1 = 0, n2 = 0, n3 = 0, n4 = 0, n5 = 0;
+    unsigned int n1 = 0, n2 = 0, n3 = 0, n4 = 0, n5 = 0, n6 = 0;
     int st = take_qmv_mma_timeouts(&n1);
     if (st != BQD_OK) return st;
     st = take_qmv_t5_timeouts(&n2);
@@ -270,7 +270,9 @@ extern "C" int bqd_device_status(bqd_stream_t stream)
     if (st != BQD_OK) return st;
     st = take_qmv_t5r_timeouts(&n5);
     if (st != BQD_OK) return st;
-    return (n1 || n2 || n3 || n4 || n5) ? BQD_ERR_TIMEOUT : BQD_OK;
+    st = kv::take_prefill_timeouts(&n6);
+    if (st != BQD_OK) return st;
+    return (n1 || n2 || n3 || n4 || n5 || n6) ? BQD_ERR_TIMEOUT : BQD_OK;
 }
 
 extern "C" int bqd_set_option(int option, int64_t value)

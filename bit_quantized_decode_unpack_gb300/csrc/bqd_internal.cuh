@@ -78,6 +78,9 @@ int take_qmv_t5_timeouts(unsigned int *count);
 int take_qmm_timeouts(unsigned int *count);
 int take_qmv_tma_timeouts(unsigned int *count);
 int take_qmv_t5r_timeouts(unsigned int *count);
+namespace kv {
+int take_prefill_timeouts(unsigned int *count);
+}
 
 // Number of SMs of the current device (cached per device).
 int sm_count();

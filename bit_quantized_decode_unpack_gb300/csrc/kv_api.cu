@@ -145,6 +145,7 @@ extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q
     a.max_len = (int)(max_len > 0 && max_len < capacity ? max_len : capacity);
     a.window = (int)(window < most ? window : 0);  // one past any position hides nothing
     a.q_vec = vec_ok(q, q_token_stride, q_head_stride);
+    if ((int64_t)a.max_new * a.group >= 64) return launch_attend_prefill(a, to_stream(stream));
     return launch_attend_decode(a, to_stream(stream));
 }
 

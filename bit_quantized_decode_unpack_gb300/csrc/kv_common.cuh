@@ -162,6 +162,7 @@ struct AppendArgs {
 
 int launch_append(const AppendArgs &a, cudaStream_t s);
 int launch_attend_decode(const AttendArgs &a, cudaStream_t s);
+int launch_attend_prefill(const AttendArgs &a, cudaStream_t s);
 int launch_reserve(const bqd_kv_cache &c, const int32_t *counts, int32_t *base, int32_t *copies, int32_t *status,
                    cudaStream_t s);
 int launch_fork(const bqd_kv_cache &from, const bqd_kv_cache &to, const int32_t *parents, const int32_t *keep,
