@@ -342,5 +342,5 @@ def device_status(stream=None) -> int:
 
 
 from . import kv_cache  # noqa: E402
-from .kv_cache import (KVCache, kv_append, kv_attend, kv_compact, kv_copy_pages, kv_fork,  # noqa: E402,F401
-                       kv_reserve)
+from .kv_cache import (KVCache, kv_append, kv_attend, kv_attend_workspace, kv_compact,  # noqa: E402,F401
+                       kv_copy_pages, kv_fork, kv_reserve)

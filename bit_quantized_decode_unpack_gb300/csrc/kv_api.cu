@@ -8,6 +8,8 @@ using namespace bqd::kv;
 
 namespace {
 
+constexpr int64_t kMaxStaged = (int64_t)8 << 30;
+
 bool at(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Status of a cache's sizes and pointers.  A cache of no rows needs no table.
@@ -80,6 +82,22 @@ bool same_pools(const bqd_kv_cache &a, const bqd_kv_cache &b)
            (!a.table || a.table != b.table) && (!a.lens || a.lens != b.lens);
 }
 
+int planned_length(const bqd_kv_cache &c, int64_t max_len)
+{
+    const int64_t capacity = (int64_t)c.row_pages * c.page_tokens;
+    return (int)(max_len > 0 && max_len < capacity ? max_len : capacity);
+}
+
+// queries enough for tiles of 128 (query, head) rows on the tensor cores
+bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group >= 64; }
+
+// bytes of scratch that a call of many queries is better with, or 0
+int64_t staged_need(const AttendArgs &a)
+{
+    const int64_t bytes = prefill_workspace(a);
+    return bytes <= kMaxStaged ? bytes : 0;
+}
+
 cudaStream_t to_stream(bqd_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 }  // namespace
@@ -112,10 +130,25 @@ extern "C" int bqd_kv_append(const bqd_kv_cache *cache, int layer, const void *k
     return launch_append(a, to_stream(stream));
 }
 
+extern "C" int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_heads, int64_t max_new, int64_t max_len)
+{
+    if (check_cache(cache) != BQD_OK) return 0;
+    const bqd_kv_cache &c = *cache;
+    if (q_heads < c.kv_heads || q_heads % c.kv_heads != 0 || max_new < 1 || max_len < 0) return 0;
+    if (max_new * (q_heads / c.kv_heads) >= (int64_t)1 << 30 || c.rows == 0) return 0;
+    AttendArgs a;
+    a.L = layer_of(c, 0);
+    a.head_dim = c.head_dim;
+    a.group = q_heads / c.kv_heads;
+    a.max_new = (int)max_new;
+    a.max_len = planned_length(c, max_len);
+    return many_queries(a) ? staged_need(a) : 0;
+}
+
 extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride,
                              int64_t q_head_stride, int dtype, int q_heads, const int32_t *starts, int64_t tokens,
                              int64_t max_new, int64_t max_len, float scale, int64_t window, void *out, float *lse,
-                             bqd_stream_t stream)
+                             void *work, int64_t work_bytes, bqd_stream_t stream)
 {
     const int st = check_cache(cache);
     if (st != BQD_OK) return st;
@@ -124,15 +157,15 @@ extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q
     if (q_heads < c.kv_heads || q_heads % c.kv_heads != 0) return BQD_ERR_INVALID_ARG;
     if (!check_tokens(c, starts, tokens, max_new) || !strides_ok(tokens, q_token_stride, q_heads, q_head_stride))
         return BQD_ERR_INVALID_ARG;
-    if (!std::isfinite(scale) || window < 0 || max_len < 0) return BQD_ERR_INVALID_ARG;
+    if (!std::isfinite(scale) || window < 0 || max_len < 0 || work_bytes < 0 || (!work && work_bytes > 0))
+        return BQD_ERR_INVALID_ARG;
     if (c.rows == 0 || tokens == 0 || max_new == 0) return BQD_OK;
     const int64_t group = q_heads / c.kv_heads, most = (int64_t)1 << 30;
     if (!starts) max_new = 1;
     if (max_new > tokens) max_new = tokens;
     if (max_new * group >= most) return BQD_ERR_INVALID_ARG;
     if (!q || !out) return BQD_ERR_INVALID_ARG;
-    if (!at(q, 2) || !at(out, 16) || !at(lse, 4) || !at(starts, 4)) return BQD_ERR_ALIGNMENT;
-    const int64_t capacity = (int64_t)c.row_pages * c.page_tokens;
+    if (!at(q, 2) || !at(out, 16) || !at(lse, 4) || !at(starts, 4) || !at(work, 16)) return BQD_ERR_ALIGNMENT;
     AttendArgs a;
     a.L = layer_of(c, layer);
     a.q = q, a.q_token = q_token_stride, a.q_head = q_head_stride;
@@ -142,11 +175,14 @@ extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q
     a.dtype = dtype, a.format = c.format, a.head_dim = c.head_dim;
     a.q_heads = q_heads, a.group = (int)group;
     a.tokens = (int)tokens, a.max_new = (int)max_new;
-    a.max_len = (int)(max_len > 0 && max_len < capacity ? max_len : capacity);
+    a.max_len = planned_length(c, max_len);
     a.window = (int)(window < most ? window : 0);  // one past any position hides nothing
     a.q_vec = vec_ok(q, q_token_stride, q_head_stride);
-    if ((int64_t)a.max_new * a.group >= 64) return launch_attend_prefill(a, to_stream(stream));
-    return launch_attend_decode(a, to_stream(stream));
+    a.work = nullptr;
+    if (!many_queries(a)) return launch_attend_decode(a, to_stream(stream));
+    const int64_t need = staged_need(a);
+    if (need > 0 && work_bytes >= need) a.work = work;
+    return launch_attend_prefill(a, to_stream(stream));
 }
 
 extern "C" int bqd_kv_reserve(const bqd_kv_cache *cache, const int32_t *counts, int32_t *base, int32_t *copies,

@@ -6,17 +6,19 @@
 //   x_ij = f s^k_b (q_i . c^k_j) + log2 s^v_b,   p_ij = 2^(x_ij - m_i),
 //   O_i = sum_j p_ij c^v_j,   l_i = sum_b (sum_{j in b} p_ij) / s^v_b,
 //   out = O / l,   lse = ln 2 (m + log2 l),
-// with m_i replaced only when a tile's maximum passes it by 8.
+// with m_i replaced only when x passes it by 15 (p < 2^15 fits fp16, and what is
+// small keeps more bits, not fewer).
 //
 // Rows of a tile are (query, head of the group) pairs, so a tile of 128 rows
 // reads each K and V code once for the whole group.  A CTA owns two tiles of
 // 128 rows (one for head_dim 256, and where there are no more rows) and walks
 // the keys in steps of KT.  Roles:
-//   warps 0-3, 4-7   softmax of tile 0 / 1: one thread a row.  S is read from
-//                    TMEM twice (maximum, then exponentials), P written over it
-//                    as fp16 in TMEM, O rescaled in TMEM when m is replaced
-//   warps 8-11       cache codes to fp16: 16-byte loads of codes for the next
-//                    step are in flight while this step's are converted into
+//   warps 0-3, 4-7   softmax of tile 0 / 1: one thread a row.  S goes from TMEM to
+//                    registers, P back over it as fp16; O is rescaled in TMEM when
+//                    m is replaced
+//   warps 8-11 (K), 13-15 (V)
+//                    cache codes to fp16: 16-byte loads of the next step's codes
+//                    are in flight while this step's are converted into
 //                    128-byte-swizzled tiles.  K and V tiles have the same
 //                    layout ([64-dim panel][key] rows of 128 bytes): K is a
 //                    K-major operand of S = Q K^T, V an MN-major one of O = P V,
@@ -29,6 +31,7 @@
 // TMEM is freed, and bqd_device_status reports it.
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "kv_common.cuh"
 #include "qmv_common.cuh"
@@ -41,14 +44,15 @@ namespace {
 using namespace qmvdev;
 using namespace tc05;
 
-constexpr int kSoftWarps = 8, kConvWarps = 4;
-constexpr int kConvThreads = kConvWarps * 32;
-constexpr int kMmaWarp = kSoftWarps + kConvWarps;
-constexpr int kThreadsF = (kMmaWarp + 1) * 32;
+constexpr int kSoftWarps = 8;
+constexpr int kMmaWarpF = 12;
+constexpr int kWarpsK = 4, kWarpsV = 3;           // warps 8-11 convert K, 13-15 V
+constexpr int kThreadsF = 512;
+constexpr int kThreadsStaged = (kSoftWarps + 2) * 32;  // warp 8 copies the staged tiles, warp 9 issues
 constexpr int kStages = 2;
 constexpr int kScaleRing = 4;  // steps whose scales are kept: a slot is written again only after
                                // both softmaxes of the step four before have finished
-constexpr float kGrow = 8.0f;
+constexpr float kGrow = 15.0f;  // p stays below 2^15, inside fp16
 
 __device__ unsigned int g_prefill_timeouts = 0;
 
@@ -69,9 +73,42 @@ struct Plan {
     static constexpr uint32_t kS1 = KT, kO0 = 256, kO1 = 256 + D, kCols = 512;
 };
 
-struct Scales {
-    float k[8], lv[8], rv[8];
-};
+// The same value, unknown to the compiler: what is computed from it is computed
+// where it is used, not kept in registers over a loop
+__device__ __forceinline__ int opaque(int x)
+{
+    asm volatile("" : "+r"(x));
+    return x;
+}
+
+__device__ __forceinline__ uint64_t two(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ float2 untwo(uint64_t x)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+    return f;
+}
+
+// two fp32 operations in one instruction, each rounded as by itself
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -80,17 +117,37 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kThreadsF, 1)
-attend_prefill_kernel(const AttendArgs a, unsigned long long wait_ns)
+// Keys [lo, lo + steps * KT) of a row that any of its n queries sees.
+struct RowSteps {
+    int lo, steps;
+    __device__ __forceinline__ RowSteps(int L, int n, int window, int KT)
+    {
+        lo = window > 0 ? max(0, L - n + 1 - window) / KT * KT : 0;
+        steps = n > 0 && L > lo ? (L - lo + KT - 1) / KT : 0;
+    }
+};
+
+// Scratch of the staged form: the K and V tiles of every step as the MMAs read
+// them, [row][head][step][K, V], then the scales of their blocks.
+struct Staged {
+    uint8_t *tiles;
+    float2 *scales;
+    int steps;      // of a row at most; 0: nothing is staged
+};
+
+template <typename T, int D, int FMT, bool STAGED>
+__global__ void __launch_bounds__(STAGED ? kThreadsStaged : kThreadsF, 1)
+attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wait_ns)
 {
     using P = Plan<D>;
     using C = Code<FMT>;
+    constexpr int kMmaWarp = STAGED ? kSoftWarps + 1 : kMmaWarpF;
+    constexpr int kFillersK = STAGED ? 1 : kWarpsK, kFillersV = STAGED ? 1 : kWarpsV;
     using H = Half2Of<T>;
     constexpr int KT = P::KT;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[4 * kStages + 9];
-    __shared__ Scales scales[kScaleRing];
+    __shared__ uint64_t bars[4 * kStages + 9 + kScaleRing];
+    __shared__ __align__(16) float2 scales[kScaleRing][8];  // of a step's blocks: K's scale, log2 of V's
     __shared__ uint32_t tmem_at;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
 
@@ -101,6 +158,9 @@ attend_prefill_kernel(const AttendArgs a, unsigned long long wait_ns)
     const int r0 = (int)(gridDim.x - 1 - blockIdx.x) * P::kRows;  // the last queries see most keys: first
     if (r0 >= rows) return;
     const int L = a.L.length(row);
+    const RowSteps all_steps(L, span.n, a.window, KT);
+    // rows that the scratch has no room for are the unstaged form's
+    if (st.steps > 0 && (all_steps.steps <= st.steps) != STAGED) return;
     const int tiles = min(P::kTiles, (rows - r0 + 127) / 128);
     const int i_min = r0 / a.group, i_max = (min(r0 + P::kRows, rows) - 1) / a.group;
     const int p_first = L - span.n;  // position of query 0
@@ -119,13 +179,14 @@ attend_prefill_kernel(const AttendArgs a, unsigned long long wait_ns)
     auto p_full = [&](int w) { return bar(4 * kStages + 3 + w); };
     auto o_full = [&](int w) { return bar(4 * kStages + 5 + w); };
     const uint32_t pv_done = bar(4 * kStages + 7), drained = bar(4 * kStages + 8);
+    auto sc_full = [&](int j) { return bar(4 * kStages + 9 + j % kScaleRing); };
 
     if (warp == kMmaWarp) {
         if (lane == 0) {
             for (int i = 0; i < kStages; ++i) {
-                mbar_init(k_full(i), kConvThreads);
+                mbar_init(k_full(i), kFillersK);
                 mbar_init(k_empty(i), 1);
-                mbar_init(v_full(i), kConvThreads);
+                mbar_init(v_full(i), kFillersV);
                 mbar_init(v_empty(i), 1);
             }
             mbar_init(q_full, 128 * tiles);
@@ -136,6 +197,7 @@ attend_prefill_kernel(const AttendArgs a, unsigned long long wait_ns)
             }
             mbar_init(pv_done, 1);
             mbar_init(drained, 1);
+            for (int i = 0; i < kScaleRing; ++i) mbar_init(sc_full(i), 1);
         }
         __syncwarp();
         tmem_alloc(smem_addr(&tmem_at), P::kCols);
@@ -206,48 +268,63 @@ attend_prefill_kernel(const AttendArgs a, unsigned long long wait_ns)
                              "r"(h[3])
                              : "memory");
             }
-            fence_proxy_async_smem();
             mbar_arrive(q_full);
 
             // ---- steps ------------------------------------------------------------
             const int p_low = p_first + (r0 + w * 128) / a.group;                               // positions of
             const int p_high = p_first + (min(r0 + w * 128 + 128, rows) - 1) / a.group;          // the tile's rows
             const uint32_t o_at = tmem + lanes + (w ? P::kO1 : P::kO0);
+            // of a block's raw scores; above 0, so that -inf (masked) stays -inf
+            auto factor = [&](float k) { return fmaxf(cs * k, 1.2e-38f); };
+            auto rescale = [&](uint32_t at, float f) {
+#pragma unroll 1
+                for (int k = 0; k < D / 16; ++k) {
+                    uint32_t o[16];
+                    ld16(at + 16 * k, o);
+                    ld_wait(o);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                    st16(at + 16 * k, o);
+                }
+            };
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int j = 0; j < steps; ++j) {
                 const int slot = pair ? w : j & 1;
                 const uint32_t s_at = tmem + lanes + (slot ? P::kS1 : 0);
-                ok = wait(s_full(slot), pair ? j : j >> 1);
+                ok = wait(sc_full(j), j / kScaleRing);
+                const float2 *sc = scales[j % kScaleRing];
+                ok = ok && wait(s_full(slot), pair ? j : j >> 1);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 fence_after();
                 const int k0 = k_lo + j * KT;
-                const Scales &sc = scales[j % kScaleRing];
                 const bool whole = k0 + KT - 1 <= p_low && (a.window == 0 || k0 > p_high - a.window);
-                const int last = pos - k0;                                          // columns <= last and
-                const int first = a.window > 0 ? pos - a.window - k0 : -1;          // > first are seen
-                // maximum
+                const int last = pos - k0, first = a.window > 0 ? last - a.window : -1;  // seen: first < i <= last
+                if constexpr (STAGED) {
+                // the row's scores in registers, its maximum, the exponentials
+                float2 v[P::kBlocks];
+#pragma unroll
+                for (int b = 0; b < P::kBlocks; ++b) v[b] = sc[b];
+                uint32_t s[KT / 32][32];
+#pragma unroll
+                for (int c = 0; c < KT / 32; ++c) ld32(s_at + 32 * c, s[c]);
+#pragma unroll
+                for (int c = 0; c < KT / 32; ++c) ld_wait(s[c]);
+                if (!whole) {
+#pragma unroll
+                    for (int i = 0; i < KT; ++i)
+                        if (i > last || i <= first) s[i / 32][i % 32] = 0xFF800000u;  // -inf
+                }
                 float mt = -INFINITY;
 #pragma unroll
-                for (int c = 0; c < KT / 32; ++c) {
-                    uint32_t s[32];
-                    ld32(s_at + 32 * c, s);
-                    ld_wait(s);
+                for (int b = 0; b < P::kBlocks; ++b) {
+                    const uint32_t *x = &s[b / 2][16 * (b & 1)];
+                    float top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        float x = -INFINITY;
-                        if (whole) {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) x = fmaxf(x, __uint_as_float(s[16 * b + i]));
-                        } else {
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const int col = 32 * c + 16 * b + i;
-                                if (col <= last && col > first) x = fmaxf(x, __uint_as_float(s[16 * b + i]));
-                            }
-                        }
-                        mt = fmaxf(mt, fmaf(x, cs * sc.k[2 * c + b], sc.lv[2 * c + b]));
-                    }
+                    for (int i = 2; i < 16; i += 2)
+                        top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                    v[b].x = factor(v[b].x);
+                    mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
                 }
                 if (__any_sync(0xffffffffu, mt > m + kGrow)) {
                     const float mn = mt > m + kGrow ? mt : m;
@@ -256,49 +333,114 @@ attend_prefill_kernel(const AttendArgs a, unsigned long long wait_ns)
                     l *= f;
                     if (j > 0) {
                         if (!pair) {
-                            ok = wait(pv_done, j - 1);  // the product of the step before still adds to O
-                            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                            // the product of the step before still adds to O
+                            ok = __all_sync(0xffffffffu, wait(pv_done, j - 1));
+                            if (!ok) break;
                             fence_after();
                         }
-#pragma unroll 1
-                        for (int c = 0; c < D / 32; ++c) {
-                            uint32_t o[32];
-                            ld32(o_at + 32 * c, o);
-                            ld_wait(o);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            st32(o_at + 32 * c, o);
-                        }
-                        st_wait();
+                        rescale(o_at, f);
                     }
                 }
                 const float ms = m == -INFINITY ? 0.0f : m;
-                // exponentials: P of columns 32c .. goes to TMEM columns 16c .., whose S is read
 #pragma unroll
-                for (int c = 0; c < KT / 32; ++c) {
-                    uint32_t s[32], p[16];
-                    ld32(s_at + 32 * c, s);
-                    ld_wait(s);
+                for (int b = 0; b < P::kBlocks; ++b) {
+                    const uint32_t *x = &s[b / 2][16 * (b & 1)];
+                    const float add = v[b].y - ms;
+                    const uint64_t ff = two(v[b].x, v[b].x), aa = two(add, add);
+                    uint64_t part = two(0.0f, 0.0f);
+                    uint32_t p[8];  // takes the place of S in TMEM, two values a column
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const float f = cs * sc.k[2 * c + b], add = sc.lv[2 * c + b] - ms;
-                        float sum = 0.0f;
+                    for (int i = 0; i < 16; i += 2) {
+                        const float2 y = untwo(fma2(two(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), ff, aa));
+                        const float e0 = ex2(y.x), e1 = ex2(y.y);
+                        part = add2(part, two(e0, e1));
+                        p[i / 2] = Half2Of<__half>::pack(e0, e1);
+                    }
+                    const float2 t = untwo(part);
+                    l = fmaf(t.x + t.y, ex2(-v[b].y), l);
+                    st8(s_at + 8 * b, p);
+                }
+                } else {
+                // Two times 32 columns in registers, each refilled as soon as it is used, in a loop
+                // that stays small: unrolled over the step, this role and the converting ones
+                // outgrow the instruction cache (measured: a third of all stalls).
+                uint32_t s0[32], s1[32];
+                bool stop = false;
+                auto columns = [&](uint32_t (&s)[32], int c) {
+                    if (!whole) {
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (32 * c + i > last || 32 * c + i <= first) s[i] = 0xFF800000u;  // -inf
+                    }
+                    const float2 va = sc[2 * c], vb = sc[2 * c + 1];
+                    const float fa = factor(va.x), fb = factor(vb.x);
+                    float ta = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+                    float tb = fmaxf(__uint_as_float(s[16]), __uint_as_float(s[17]));
+#pragma unroll
+                    for (int i = 2; i < 16; i += 2) {
+                        ta = fmaxf(fmaxf(ta, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+                        tb = fmaxf(fmaxf(tb, __uint_as_float(s[16 + i])), __uint_as_float(s[17 + i]));
+                    }
+                    const float mt = fmaxf(fmaf(ta, fa, va.y), fmaf(tb, fb, vb.y));
+                    if (__any_sync(0xffffffffu, mt > m + kGrow)) {
+                        // a new reference, a whole power of two away: l, this step's P so far and O follow
+                        const float mn = mt > m + kGrow ? (m == -INFINITY ? mt : m + ceilf(mt - m)) : m;
+                        const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+                        m = mn;
+                        l *= f;
+                        st_wait();
+#pragma unroll 1
+                        for (int k = 0; k < c; ++k) {
+                            uint32_t p[16];
+                            ld16(s_at + 16 * k, p);
+                            ld_wait(p);
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const float2 v = Half2Of<__half>::f2(p[i]);  // f itself may be below fp16's range
+                                p[i] = Half2Of<__half>::pack(v.x * f, v.y * f);
+                            }
+                            st16(s_at + 16 * k, p);
+                        }
+                        if (j > 0 && !pair && !stop) {
+                            // the product of the step before still adds to O
+                            stop = !__all_sync(0xffffffffu, wait(pv_done, j - 1));
+                            fence_after();
+                        }
+                        if (j > 0 && !stop) rescale(o_at, f);
+                    }
+                    const float ms = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[8];  // takes the place of S in TMEM, two values a column
+                        const float f = h ? fb : fa, lv = h ? vb.y : va.y, add = lv - ms;
+                        const uint64_t ff = two(f, f), aa = two(add, add);
+                        uint64_t part = two(0.0f, 0.0f);
 #pragma unroll
                         for (int i = 0; i < 16; i += 2) {
-                            float x0 = fmaf(__uint_as_float(s[16 * b + i]), f, add);
-                            float x1 = fmaf(__uint_as_float(s[16 * b + i + 1]), f, add);
-                            if (!whole) {
-                                const int col = 32 * c + 16 * b + i;
-                                if (col > last || col <= first) x0 = -INFINITY;
-                                if (col + 1 > last || col + 1 <= first) x1 = -INFINITY;
-                            }
-                            const float e0 = ex2(x0), e1 = ex2(x1);
-                            sum += e0 + e1;
-                            p[8 * b + i / 2] = Half2Of<__half>::pack(e0, e1);
+                            const float2 x = untwo(fma2(two(__uint_as_float(s[16 * h + i]),
+                                                            __uint_as_float(s[16 * h + i + 1])), ff, aa));
+                            const float e0 = ex2(x.x), e1 = ex2(x.y);
+                            part = add2(part, two(e0, e1));
+                            p[i / 2] = Half2Of<__half>::pack(e0, e1);
                         }
-                        l = fmaf(sum, sc.rv[2 * c + b], l);
+                        const float2 t = untwo(part);
+                        l = fmaf(t.x + t.y, ex2(-lv), l);
+                        st8(s_at + 16 * c + 8 * h, p);
                     }
-                    st16(s_at + 16 * c, p);
+                };
+                constexpr int kChunks = KT / 32;
+                ld32(s_at, s0);
+                ld32(s_at + 32, s1);
+#pragma unroll 1
+                for (int c = 0; c < kChunks; c += 2) {
+                    ld_wait(s0);
+                    ld_wait(s1);
+                    columns(s0, c);
+                    if (c + 2 < kChunks) ld32(s_at + 32 * (c + 2), s0);
+                    columns(s1, c + 1);
+                    if (c + 2 < kChunks) ld32(s_at + 32 * (c + 3), s1);
+                }
+                if (stop) { ok = false; break; }
                 }
                 st_wait();
                 fence_before();
@@ -337,129 +479,164 @@ attend_prefill_kernel(const AttendArgs a, unsigned long long wait_ns)
                         l == 0.0f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
             }
         }
-    } else if (warp < kMmaWarp) {
+    } else if (warp != kMmaWarp) {
         // ---- codes to fp16 tiles ---------------------------------------------------
-        // four lanes take the 64 bytes of a key's panel, eight keys a warp: the 16-byte
-        // stores of a quarter warp (two keys) hit all banks once
-        constexpr int kGroups = KT / 32;  // keys of a thread in each panel: gi * 32 + key
-        const int ct = tid - kSoftWarps * 32, key = ct >> 2, part = ct & 3;
-        uint4 kx[kGroups * P::kPanels], vx[kGroups * P::kPanels];
-        int64_t blk[kGroups];
-        auto find = [&](int j) {
+        // An item is one panel (64 dims) of eight keys: four lanes take the 64 bytes of a
+        // key, so that the 16-byte stores of a quarter warp (two keys) hit all banks once.
+        // The warps take the items of a tile in turn.
+        // Loads run one step ahead of the conversion and page ids one ahead of the loads, so
+        // that no load's address waits for another load.  Lane b < KT / 16 keeps the place of
+        // the step's block b; the others get it by shuffle.
+        constexpr int kItems = P::kPanels * KT / 8;
+        const int part = lane & 3, sub = lane >> 2;
+        auto convert = [&](auto warps, int cw, const uint8_t *pool, uint32_t tile0, auto full, auto empty, bool is_k) {
+            constexpr int kW = decltype(warps)::value, kEach = (kItems + kW - 1) / kW;
+            const bool scaler = is_k && cw == 0;
+            uint4 x[kEach];
+            int page = 0;         // of the step after the next, as listed
+            int64_t place = 0;    // of the next step: index of the block in the layer's pool
+            float ksc = 1.0f, vsc = 1.0f;
+            auto look_up = [&](int j) {
+                const int t = k_lo + j * KT + lane * kBlock;
+                page = lane < P::kBlocks && t < hi ? a.L.listed(row, t) : 0;
+            };
+            auto load = [&](int j) {
+                const int k0 = k_lo + j * KT;
+                place = a.L.block_at((unsigned)page < (unsigned)a.L.pages ? page : 0, head, k0 + lane * kBlock);
+                look_up(j + 1);
+                const int c0 = opaque(cw);
 #pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi) {
-                const int t = k_lo + j * KT + gi * 32 + key;
-                blk[gi] = t < hi ? a.L.block_of(row, head, t) : -1;
-            }
-        };
-        auto load = [&](const uint8_t *pool, uint4 (&x)[kGroups * P::kPanels]) {
-#pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi)
-#pragma unroll
-                for (int p = 0; p < P::kPanels; ++p) {
-                    uint4 v = make_uint4(0, 0, 0, 0);  // keys past the last that is seen: 0, never stale bytes
-                    if (blk[gi] >= 0)
-                        v = __ldg(reinterpret_cast<const uint4 *>(pool + blk[gi] * (kBlock * D) + (key & 15) * D +
-                                                                  p * 64 + part * 16));
-                    x[gi * P::kPanels + p] = v;
+                for (int i = 0; i < kEach; ++i) {
+                    const int item = c0 + i * kW, eight = item % (KT / 8);
+                    const int64_t b = __shfl_sync(0xffffffffu, place, eight >> 1);
+                    // keys past the last that is seen: 0, never stale bytes
+                    x[i] = ld_stream_v4_if(
+                        pool + b * (kBlock * D) + ((eight & 1) * 8 + sub) * D + item / (KT / 8) * 64 + part * 16,
+                        item < kItems && k0 + eight * 8 + sub < hi);
                 }
-        };
-        auto store = [&](uint32_t tile, const uint4 (&x)[kGroups * P::kPanels]) {
+                ksc = vsc = 1.0f;
+                if (scaler && lane < P::kBlocks && k0 + lane * kBlock < hi) {
+                    ksc = __ldg(a.L.ks + place);
+                    vsc = __ldg(a.L.vs + place);
+                }
+            };
+            look_up(0);
+            load(0);
+            for (int j = 0; j < steps; ++j) {
+                bool ok = true;
+                if (j >= kStages) ok = wait(empty(j), j / kStages - 1);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                if (scaler) {
+                    const float v = fmaxf(vsc, 1e-37f);
+                    if (lane < P::kBlocks)
+                        scales[j % kScaleRing][lane] = make_float2(ksc, __log2f(v));
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(sc_full(j));
+                }
+                const uint32_t tile = tile0 + (j % kStages) * P::kKV;
+                const int c0 = opaque(cw);
 #pragma unroll
-            for (int gi = 0; gi < kGroups; ++gi)
-#pragma unroll
-                for (int p = 0; p < P::kPanels; ++p) {
-                    const int kk = gi * 32 + key;
-                    const uint32_t at = tile + p * P::kPanelKV + kk * 128;
-                    const uint4 v = x[gi * P::kPanels + p];
-                    const uint32_t w[4] = {C::ready(v.x), C::ready(v.y), C::ready(v.z), C::ready(v.w)};
+                for (int i = 0; i < kEach; ++i) {
+                    const int item = c0 + i * kW, key = item % (KT / 8) * 8 + sub;
+                    if (item >= kItems) break;
+                    const uint32_t to = tile + item / (KT / 8) * P::kPanelKV + key * 128;
+                    const uint32_t w[4] = {C::ready(x[i].x), C::ready(x[i].y), C::ready(x[i].z), C::ready(x[i].w)};
 #pragma unroll
                     for (int h = 0; h < 2; ++h)
-                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         at + (((2 * part + h) ^ (kk & 7)) << 4)),
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(to + (((2 * part + h) ^ sub) << 4)),
                                      "r"(C::template pair<0>(w[2 * h])), "r"(C::template pair<1>(w[2 * h])),
                                      "r"(C::template pair<0>(w[2 * h + 1])), "r"(C::template pair<1>(w[2 * h + 1]))
                                      : "memory");
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(full(j));
+                load(j + 1);  // past the end: nothing is read
+            }
         };
-        bool ok = true;
-        if (steps > 0) {
-            find(0);
-            load(a.L.k, kx);
-        }
-        for (int j = 0; j < steps && ok; ++j) {
-            load(a.L.v, vx);
-            float ksc = 0.0f, vsc = 1.0f;
-            if (ct < P::kBlocks) {
-                const int t = k_lo + j * KT + ct * kBlock;
-                if (t < hi) {
-                    const int64_t b = a.L.block_of(row, head, t);
-                    ksc = __ldg(a.L.ks + b);
-                    vsc = fmaxf(__ldg(a.L.vs + b), 1e-37f);
+        if constexpr (STAGED) {
+            // ---- copies of staged tiles -------------------------------------------------
+            if (lane == 0) {
+                const int64_t first = ((int64_t)row * a.L.heads + head) * st.steps + (k_lo - all_steps.lo) / KT;
+                int j = 0, v_issued = 0;
+                for (; j < steps; ++j) {
+                    const uint8_t *tile = st.tiles + (first + j) * (2 * P::kKV);
+                    if (j >= kStages && !wait(k_empty(j), j / kStages - 1)) break;
+                    mbar_arrive_expect_tx(sc_full(j), P::kBlocks * 8);
+                    bulk_g2s(smem_addr(scales[j % kScaleRing]), st.scales + (first + j) * P::kBlocks, P::kBlocks * 8, sc_full(j));
+                    mbar_arrive_expect_tx(k_full(j), P::kKV);
+                    bulk_g2s(base + P::kOffK + (j % kStages) * P::kKV, tile, P::kKV, k_full(j));
+                    if (j >= kStages && !wait(v_empty(j), j / kStages - 1)) {
+                        ++j;
+                        break;
+                    }
+                    mbar_arrive_expect_tx(v_full(j), P::kKV);
+                    bulk_g2s(base + P::kOffV + (j % kStages) * P::kKV, tile + P::kKV, P::kKV, v_full(j));
+                    v_issued = j + 1;
+                }
+                // nothing of this CTA's is in flight when it leaves
+                for (int i = max(0, j - kStages); i < j; ++i) {
+                    mbar_wait_for(k_full(i), (i / kStages) & 1, kDrainWaitNs, &g_prefill_timeouts);
+                    if (i < v_issued) mbar_wait_for(v_full(i), (i / kStages) & 1, kDrainWaitNs, &g_prefill_timeouts);
+                    mbar_wait_for(sc_full(i), (i / kScaleRing) & 1, kDrainWaitNs, &g_prefill_timeouts);
                 }
             }
-            if (j >= kStages) ok = wait(k_empty(j), j / kStages - 1);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            if (ct < P::kBlocks) {
-                Scales &sc = scales[j % kScaleRing];
-                sc.k[ct] = ksc;
-                sc.lv[ct] = __log2f(vsc);
-                sc.rv[ct] = __frcp_rn(vsc);
-            }
-            store(base + P::kOffK + (j % kStages) * P::kKV, kx);
-            fence_proxy_async_smem();
-            mbar_arrive(k_full(j));
-            if (j + 1 < steps) {
-                find(j + 1);
-                load(a.L.k, kx);
-            }
-            if (j >= kStages) ok = wait(v_empty(j), j / kStages - 1);
-            if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
-            store(base + P::kOffV + (j % kStages) * P::kKV, vx);
-            fence_proxy_async_smem();
-            mbar_arrive(v_full(j));
+        } else if (steps > 0) {
+            if (warp < kMmaWarp)
+                convert(std::integral_constant<int, kWarpsK>(), warp - kSoftWarps, a.L.k, base + P::kOffK, k_full, k_empty, true);
+            else
+                convert(std::integral_constant<int, kWarpsV>(), warp - kMmaWarp - 1, a.L.v, base + P::kOffV, v_full, v_empty, false);
         }
-    } else if (lane == 0) {
-        // ---- MMA issue --------------------------------------------------------------
-        constexpr uint32_t i_qk = idesc_f16(128, KT, false), i_pv = idesc_f16(128, D, true);
+    } else {
+        // ---- MMA issue: the warp runs converged, one elected lane issues ---------------
+        constexpr uint32_t i_qk = idesc_f16(128, KT, false), i_pv = idesc_f16(128, D, true), hi_word = desc128_hi(1024);
+        const uint32_t q_lo = desc128_lo(base, 16), k_lo_word = desc128_lo(base + P::kOffK, 16);
+        const uint32_t v_lo = desc128_lo(base + P::kOffV, P::kPanelKV);
         auto qk = [&](int j, int w, int slot) {
-            const uint32_t q = base + w * (P::kPanels * P::kPanelQ), k = base + P::kOffK + (j % kStages) * P::kKV;
+            const uint32_t q = q_lo + w * (P::kPanels * P::kPanelQ / 16), k = k_lo_word + (j % kStages) * (P::kKV / 16);
 #pragma unroll
             for (int s = 0; s < D / 16; ++s)
-                mma_ss(tmem + (slot ? P::kS1 : 0), desc128(q + (s / 4) * P::kPanelQ + (s % 4) * 32, 16, 1024),
-                       desc128(k + (s / 4) * P::kPanelKV + (s % 4) * 32, 16, 1024), i_qk, s > 0);
+                mma_ss(tmem + (slot ? P::kS1 : 0), q + ((s / 4) * P::kPanelQ + (s % 4) * 32) / 16, hi_word,
+                       k + ((s / 4) * P::kPanelKV + (s % 4) * 32) / 16, hi_word, i_qk, s > 0);
             commit(s_full(slot));
         };
         auto pv = [&](int j, int w, int slot) {
-            const uint32_t v = base + P::kOffV + (j % kStages) * P::kKV;
+            const uint32_t v = v_lo + (j % kStages) * (P::kKV / 16);
 #pragma unroll
             for (int s = 0; s < KT / 16; ++s)
-                mma_ts(tmem + (w ? P::kO1 : P::kO0), tmem + (slot ? P::kS1 : 0) + 8 * s,
-                       desc128(v + s * 16 * 128, P::kPanelKV, 1024), i_pv, j > 0 || s > 0);
+                mma_ts(tmem + (w ? P::kO1 : P::kO0), tmem + (slot ? P::kS1 : 0) + 8 * s, v + s * (16 * 128 / 16), hi_word,
+                       i_pv, j > 0 || s > 0);
         };
-        bool ok = steps > 0 && wait(q_full, 0) && wait(k_full(0), 0);
-        if (ok) {
+        // The tiles are written by ordinary stores and read by the MMAs: the fence between the two
+        // stands here, after the wait, because the writers have loads in flight that a fence of
+        // theirs would wait for.
+        auto filled = [&] {
             fence_after();
+            fence_proxy_async_smem();
+        };
+        auto all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+        bool ok = steps > 0 && all(q_full, 0) && all(k_full(0), 0);
+        if (ok) {
+            filled();
             qk(0, 0, 0);
             if (pair) qk(0, 1, 1);
             commit(k_empty(0));
         }
         for (int j = 0; j < steps && ok; ++j) {
             const bool next = j + 1 < steps;
+            // the tiles of this step's second product and of the next step's first, and their
+            // fence, before the wait for P that everything here follows
+            if (pair) ok = all(v_full(j), j / kStages);
+            if (ok && next) ok = all(k_full(j + 1), (j + 1) / kStages);
+            if (!ok) break;
+            filled();
             if (pair) {
-                ok = wait(v_full(j), j / kStages) && wait(p_full(0), j);
+                ok = all(p_full(0), j);
                 if (!ok) break;
                 fence_after();
                 pv(j, 0, 0);
-                if (next) {
-                    ok = wait(k_full(j + 1), (j + 1) / kStages);
-                    if (!ok) break;
-                    fence_after();
-                    qk(j + 1, 0, 0);
-                } else {
-                    commit(o_full(0));
-                }
-                ok = wait(p_full(1), j);
+                if (next) qk(j + 1, 0, 0);
+                else commit(o_full(0));
+                ok = all(p_full(1), j);
                 if (!ok) break;
                 fence_after();
                 pv(j, 1, 1);
@@ -472,13 +649,13 @@ attend_prefill_kernel(const AttendArgs a, unsigned long long wait_ns)
                 }
             } else {
                 if (next) {
-                    ok = wait(k_full(j + 1), (j + 1) / kStages);
-                    if (!ok) break;
-                    fence_after();
                     qk(j + 1, 0, (j + 1) & 1);
                     commit(k_empty(j + 1));
                 }
-                ok = wait(v_full(j), j / kStages) && wait(p_full(j & 1), j >> 1);
+                ok = all(v_full(j), j / kStages);
+                if (!ok) break;
+                filled();
+                ok = all(p_full(j & 1), j >> 1);
                 if (!ok) break;
                 fence_after();
                 pv(j, 0, j & 1);
@@ -499,22 +676,103 @@ attend_prefill_kernel(const AttendArgs a, unsigned long long wait_ns)
     if (warp == kMmaWarp) tmem_dealloc(tmem, P::kCols);
 }
 
+// Codes to fp16 tiles for the staged form: one CTA a tile (K or V of one step),
+// as the MMAs will read it; the codes of a row are converted once for all of
+// its query tiles.
+template <int D, int FMT>
+__global__ void __launch_bounds__(256)
+stage_kernel(const AttendArgs a, const Staged st)
+{
+    using P = Plan<D>;
+    using C = Code<FMT>;
+    constexpr int KT = P::KT, kChunks = D / 16;  // 16-byte pieces of a token
+    const int j = blockIdx.x >> 1, which = blockIdx.x & 1, head = blockIdx.y, row = blockIdx.z;
+    const Span span(a.starts, row, a.tokens, a.max_new);
+    const int L = a.L.length(row);
+    const RowSteps all(L, span.n, a.window, KT);
+    if (j >= all.steps || all.steps > st.steps) return;
+    const int k0 = all.lo + j * KT;
+    const int64_t step = ((int64_t)row * a.L.heads + head) * st.steps + j;
+    uint8_t *tile = st.tiles + (2 * step + which) * P::kKV;
+    const uint8_t *pool = which ? a.L.v : a.L.k;
+    constexpr int kEach = KT * kChunks / 256;
+    uint4 x[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int at = threadIdx.x + i * 256, key = at / kChunks, t = k0 + key;
+        x[i] = make_uint4(0, 0, 0, 0);  // keys past the row: 0, never stale bytes
+        if (t < L)
+            x[i] = __ldg(reinterpret_cast<const uint4 *>(pool + a.L.block_of(row, head, t) * (kBlock * D) + (t & 15) * D +
+                                                         (at % kChunks) * 16));
+    }
+    if (which == 0 && threadIdx.x < P::kBlocks) {
+        const int t = k0 + threadIdx.x * kBlock;
+        float2 s = make_float2(1.0f, 0.0f);
+        if (t < L) {
+            const int64_t b = a.L.block_of(row, head, t);
+            s = make_float2(__ldg(a.L.ks + b), __log2f(fmaxf(__ldg(a.L.vs + b), 1e-37f)));
+        }
+        st.scales[step * P::kBlocks + threadIdx.x] = s;
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) {
+        const int at = threadIdx.x + i * 256, key = at / kChunks, c = at % kChunks;
+        uint8_t *to = tile + (c / 4) * P::kPanelKV + key * 128;
+        const uint32_t w[4] = {C::ready(x[i].x), C::ready(x[i].y), C::ready(x[i].z), C::ready(x[i].w)};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            *reinterpret_cast<uint4 *>(to + ((((c % 4) * 2 + h) ^ (key & 7)) << 4)) =
+                make_uint4(C::template pair<0>(w[2 * h]), C::template pair<1>(w[2 * h]), C::template pair<0>(w[2 * h + 1]),
+                           C::template pair<1>(w[2 * h + 1]));
+    }
+}
+
+template <typename K>
+bool configure(K kern, size_t smem, bool (&done)[64])
+{
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev >= 0 && dev < 64 && done[dev]) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) return false;
+    if (dev >= 0 && dev < 64) done[dev] = true;
+    return true;
+}
+
+// Steps of a row that the scratch is laid out for, and its bytes
+template <int D>
+int staged_steps(const AttendArgs &a)
+{
+    return a.max_len / Plan<D>::KT + 2;  // a window's first step may start before its keys
+}
+template <int D>
+int64_t staged_bytes(const AttendArgs &a)
+{
+    using P = Plan<D>;
+    return (int64_t)a.L.rows * a.L.heads * staged_steps<D>(a) * (2 * (int64_t)P::kKV + P::kBlocks * 8);
+}
+
 template <typename T, int D, int FMT>
 int launch_t(const AttendArgs &a, cudaStream_t s)
 {
     using P = Plan<D>;
-    auto kern = attend_prefill_kernel<T, D, FMT>;
-    static bool done[64] = {};
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return BQD_ERR_CUDA;
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)P::kSmem) != cudaSuccess)
-            return BQD_ERR_CUDA;
-        if (dev >= 0 && dev < 64) done[dev] = true;
-    }
+    auto direct = attend_prefill_kernel<T, D, FMT, false>;
+    auto staged = attend_prefill_kernel<T, D, BQD_KV_INT8, true>;  // its tiles are fp16 in either format
+    static bool done[2][64] = {};
+    if (!configure(direct, P::kSmem, done[0]) || !configure(staged, P::kSmem, done[1])) return BQD_ERR_CUDA;
     const int64_t rows = (int64_t)a.max_new * a.group;
     const dim3 grid((unsigned)((rows + P::kRows - 1) / P::kRows), (unsigned)a.L.heads, (unsigned)a.L.rows);
-    kern<<<grid, kThreadsF, P::kSmem, s>>>(a, opt_wait_ns());
+    Staged st = {nullptr, nullptr, 0};
+    if (a.work) {
+        st.steps = staged_steps<D>(a);
+        const int64_t tiles = (int64_t)a.L.rows * a.L.heads * st.steps;
+        st.tiles = static_cast<uint8_t *>(a.work);
+        st.scales = reinterpret_cast<float2 *>(st.tiles + tiles * 2 * P::kKV);
+        stage_kernel<D, FMT><<<dim3(2 * st.steps, a.L.heads, a.L.rows), 256, 0, s>>>(a, st);
+        staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, opt_wait_ns());
+        // a row can only be longer than planned where the plan is below the table's capacity
+        if ((int64_t)a.max_len >= ((int64_t)a.L.row_pages << a.L.page_shift)) return cuda_status(cudaGetLastError());
+    }
+    direct<<<grid, kThreadsF, P::kSmem, s>>>(a, st, opt_wait_ns());
     return cuda_status(cudaGetLastError());
 }
 
@@ -527,6 +785,11 @@ int launch_d(const AttendArgs &a, cudaStream_t s)
 }
 
 }  // namespace
+
+int64_t prefill_workspace(const AttendArgs &a)
+{
+    return a.head_dim == 64 ? staged_bytes<64>(a) : a.head_dim == 128 ? staged_bytes<128>(a) : staged_bytes<256>(a);
+}
 
 int launch_attend_prefill(const AttendArgs &a, cudaStream_t s)
 {

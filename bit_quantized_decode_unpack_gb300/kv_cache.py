@@ -49,13 +49,16 @@ def declare(lib):
     """Argument types of the cache's entry points."""
     i64, i32, vp, cp = ctypes.c_int64, ctypes.c_int, ctypes.c_void_p, ctypes.POINTER(CacheStruct)
     lib.bqd_kv_append.argtypes = [cp, i32, vp, i64, i64, vp, i64, i64, i32, vp, vp, i64, i64, vp]
-    lib.bqd_kv_attend.argtypes = [cp, i32, vp, i64, i64, i32, i32, vp, i64, i64, i64, ctypes.c_float, i64, vp, vp, vp]
+    lib.bqd_kv_attend.argtypes = [cp, i32, vp, i64, i64, i32, i32, vp, i64, i64, i64, ctypes.c_float, i64, vp, vp, vp,
+                                  i64, vp]
+    lib.bqd_kv_attend_workspace.argtypes = [cp, i32, i64, i64]
     lib.bqd_kv_reserve.argtypes = [cp, vp, vp, vp, vp, vp]
     lib.bqd_kv_fork.argtypes = [cp, cp, vp, vp, vp]
     lib.bqd_kv_compact.argtypes = [cp, cp, vp, vp, vp]
     lib.bqd_kv_copy_pages.argtypes = [cp, vp, vp, i64, vp]
     for f in ("append", "attend", "reserve", "fork", "compact", "copy_pages"):
         getattr(lib, f"bqd_kv_{f}").restype = i32
+    lib.bqd_kv_attend_workspace.restype = i64
 
 
 def _dense(t, name, dtype, shape, device):
@@ -262,11 +265,19 @@ class KVCache:
             lse = torch.empty((tokens, heads), dtype=torch.float32, device=self.device)
         else:
             _dense(lse, "lse", torch.float32, (tokens, heads), self.device)
+        # scratch, from the allocator's pool of this stream: used by this call alone
+        need = self.attend_workspace(heads, max_new, max_len) if max_new * heads >= 64 else 0
+        work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         qs = q.stride()
         _check("bqd_kv_attend", self._lib.bqd_kv_attend(
             self._ref, self._layer(layer), q.data_ptr(), qs[0], qs[1], kind, heads, at, tokens, max_new, max_len,
-            1.0 / math.sqrt(d) if scale is None else scale, window, out.data_ptr(), lse.data_ptr(), self._stream()))
+            1.0 / math.sqrt(d) if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
+            work.data_ptr() if need else None, need, self._stream()))
         return out, lse
+
+    def attend_workspace(self, q_heads: int, max_new: int, max_len: int = 0) -> int:
+        """Bytes of scratch that ``attend`` takes for such a call (bqd_kv_attend_workspace)."""
+        return self._lib.bqd_kv_attend_workspace(self._ref, q_heads, max_new, max_len)
 
     # ---- pages -------------------------------------------------------------------
 
@@ -355,4 +366,5 @@ class KVCache:
 
 # the entry points' names, as functions of a cache
 kv_append, kv_attend, kv_reserve = KVCache.append, KVCache.attend, KVCache.reserve
+kv_attend_workspace = KVCache.attend_workspace
 kv_fork, kv_compact, kv_copy_pages = KVCache.fork, KVCache.compact, KVCache.copy_pages

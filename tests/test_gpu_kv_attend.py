@@ -201,6 +201,14 @@ def test_the_same_call_gives_the_same_bits():
             np.testing.assert_array_equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("n", [1, 9, 150])
+def test_a_scale_of_zero_is_a_mean(n):
+    rng = np.random.default_rng(15)
+    c = random_cache(rng, [210, n], heads=1, d=64, pt=32)
+    q, qd = rounded(rng.standard_normal((2 * n, 2, 64)), "float16")
+    _compare(c, q, qd, [n, n], "float16", scale=0.0, window=100)
+
+
 def test_layers_scale_given_outputs_and_untouched_rows():
     import torch
     rng = np.random.default_rng(11)

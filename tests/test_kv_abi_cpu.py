@@ -25,10 +25,10 @@ def _cache(**kw):
 
 
 def _attend(lib, c=None, layer=0, q=0x1000, ts=512, hs=128, dt=1, heads=4, starts=None, tokens=3, max_new=1, max_len=0,
-            scale=0.1, window=0, out=0x2000, lse=None):
+            scale=0.1, window=0, out=0x2000, lse=None, work=None, work_bytes=0):
     c = c or _cache()
     return lib.bqd_kv_attend(ctypes.byref(c), layer, q, ts, hs, dt, heads, starts, tokens, max_new, max_len, scale,
-                             window, out, lse, None)
+                             window, out, lse, work, work_bytes, None)
 
 
 def test_struct_layout_matches_the_header():
@@ -66,6 +66,7 @@ def test_null_cache(lib):
     (dict(out=None), INV), (dict(scale=float("inf")), INV), (dict(scale=float("nan")), INV), (dict(window=-1), INV),
     (dict(max_len=-1), INV), (dict(ts=-1), INV), (dict(hs=1 << 41), INV), (dict(q=0x1001), ALIGN),
     (dict(out=0x2008), ALIGN), (dict(lse=0x2002), ALIGN), (dict(starts=0x4002), ALIGN),
+    (dict(work_bytes=-1), INV), (dict(work_bytes=16), INV), (dict(work=0x9008, work_bytes=16), ALIGN),
     (dict(starts=0x4000, tokens=0, q=None, out=None), 0), (dict(starts=0x4000, max_new=0, q=None), 0),
 ])
 def test_attend(lib, kw, want):
@@ -83,6 +84,17 @@ def test_append(lib, kw, want):
     c = _cache()
     assert lib.bqd_kv_append(ctypes.byref(c), a["layer"], a["k"], a["ts"], a["hs"], a["v"], a["ts"], a["hs"], a["dt"],
                              a["base"], a["starts"], a["tokens"], a["max_new"], None) == want
+
+
+def test_workspace(lib):
+    r = ctypes.byref(_cache())
+    w = lib.bqd_kv_attend_workspace
+    assert w(r, 4, 1, 0) == 0                                    # few queries need none
+    assert w(r, 4, 4096, 200) >= 3 * 2 * 200 * 2 * 128 * 2       # fp16 K and V of every row and head
+    assert w(r, 4, 4096, 100) < w(r, 4, 4096, 256) == w(r, 4, 4096, 0) == w(r, 4, 4096, 10 ** 9)
+    for bad in ((r, 3, 4096, 0), (r, 0, 4096, 0), (r, 4, 0, 0), (r, 4, 4096, -1), (r, 4, 1 << 40, 0),
+                (ctypes.byref(_cache(pages=0)), 4, 4096, 0), (None, 4, 4096, 0)):
+        assert w(*bad) == 0
 
 
 def test_pages(lib):
