@@ -29,8 +29,11 @@
 // step is computed during the softmax of this one.
 // Every wait is bounded; on expiry a role stops, what it issued is drained,
 // TMEM is freed, and bqd_device_status reports it.
+#include <cudaTypedefs.h>
+
 #include <algorithm>
 #include <cmath>
+#include <mutex>
 #include <type_traits>
 
 #include "kv_common.cuh"
@@ -72,6 +75,15 @@ struct Plan {
     // TMEM columns
     static constexpr uint32_t kS1 = KT, kO0 = 256, kO1 = 256 + D, kCols = 512;
 };
+
+__device__ __forceinline__ void tma_load_2d(uint32_t dst, const CUtensorMap *map, int c0, int c1, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+            dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(c0), "r"(c1), "r"(bar)
+        : "memory");
+}
 
 // The same value, unknown to the compiler: what is computed from it is computed
 // where it is used, not kept in registers over a loop
@@ -137,7 +149,8 @@ struct Staged {
 
 template <typename T, int D, int FMT, bool STAGED>
 __global__ void __launch_bounds__(STAGED ? kThreadsStaged : kThreadsF, 1)
-attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wait_ns)
+attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant__ CUtensorMap map,
+                      unsigned long long wait_ns)
 {
     using P = Plan<D>;
     using C = Code<FMT>;
@@ -146,7 +159,7 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wa
     using H = Half2Of<T>;
     constexpr int KT = P::KT;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t bars[4 * kStages + 9 + kScaleRing];
+    __shared__ uint64_t bars[4 * kStages + 13 + kScaleRing];
     __shared__ __align__(16) float2 scales[kScaleRing][8];  // of a step's blocks: K's scale, log2 of V's
     __shared__ uint32_t tmem_at;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -176,10 +189,11 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wa
     auto v_empty = [&](int j) { return bar(3 * kStages + j % kStages); };
     const uint32_t q_full = bar(4 * kStages);
     auto s_full = [&](int w) { return bar(4 * kStages + 1 + w); };
-    auto p_full = [&](int w) { return bar(4 * kStages + 3 + w); };
+    auto p_full = [&](int w, int half) { return bar(half ? 4 * kStages + 9 + w : 4 * kStages + 3 + w); };
+    auto pv_half = [&](int w) { return bar(4 * kStages + 11 + w); };
     auto o_full = [&](int w) { return bar(4 * kStages + 5 + w); };
     const uint32_t pv_done = bar(4 * kStages + 7), drained = bar(4 * kStages + 8);
-    auto sc_full = [&](int j) { return bar(4 * kStages + 9 + j % kScaleRing); };
+    auto sc_full = [&](int j) { return bar(4 * kStages + 13 + j % kScaleRing); };
 
     if (warp == kMmaWarp) {
         if (lane == 0) {
@@ -192,7 +206,9 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wa
             mbar_init(q_full, 128 * tiles);
             for (int w = 0; w < 2; ++w) {
                 mbar_init(s_full(w), 1);
-                mbar_init(p_full(w), 128);
+                mbar_init(p_full(w, 0), 128);
+                mbar_init(p_full(w, 1), 128);
+                mbar_init(pv_half(w), 1);
                 mbar_init(o_full(w), 1);
             }
             mbar_init(pv_done, 1);
@@ -276,175 +292,108 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wa
             const uint32_t o_at = tmem + lanes + (w ? P::kO1 : P::kO0);
             // of a block's raw scores; above 0, so that -inf (masked) stays -inf
             auto factor = [&](float k) { return fmaxf(cs * k, 1.2e-38f); };
-            auto rescale = [&](uint32_t at, float f) {
-#pragma unroll 1
-                for (int k = 0; k < D / 16; ++k) {
-                    uint32_t o[16];
-                    ld16(at + 16 * k, o);
-                    ld_wait(o);
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                    st16(at + 16 * k, o);
-                }
-            };
             float m = -INFINITY, l = 0.0f;
             bool ok = true;
             for (int j = 0; j < steps; ++j) {
                 const int slot = pair ? w : j & 1;
                 const uint32_t s_at = tmem + lanes + (slot ? P::kS1 : 0);
+                // the blocks' scales while S is on its way: shared memory answers slowly (300 to 400
+                // cycles) while the MMAs read their operands from it
                 ok = wait(sc_full(j), j / kScaleRing);
-                const float2 *sc = scales[j % kScaleRing];
+                float2 sc[P::kBlocks];
+#pragma unroll
+                for (int b = 0; b < P::kBlocks; ++b) {
+                    sc[b] = scales[j % kScaleRing][b];
+                    sc[b].x = factor(sc[b].x);
+                }
                 ok = ok && wait(s_full(slot), pair ? j : j >> 1);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                 fence_after();
                 const int k0 = k_lo + j * KT;
                 const bool whole = k0 + KT - 1 <= p_low && (a.window == 0 || k0 > p_high - a.window);
                 const int last = pos - k0, first = a.window > 0 ? last - a.window : -1;  // seen: first < i <= last
-                if constexpr (STAGED) {
-                // the row's scores in registers, its maximum, the exponentials
-                float2 v[P::kBlocks];
+                // Half of the step's columns at a time: the MMAs of the first half's P run while the
+                // second half is computed.  Exponentials are taken against the reference that is
+                // there, with the half's maximum found beside them; where a row passes its reference
+                // by too much (the first step, seldom after it) the warp replaces it and computes
+                // the half again.  P takes the place of scores that were read, two values a column.
+                constexpr int kHalf = KT / 2, kHalfBlocks = kHalf / 16, kChunks = kHalf / 32;
+                uint32_t s[2][kChunks][32];
 #pragma unroll
-                for (int b = 0; b < P::kBlocks; ++b) v[b] = sc[b];
-                uint32_t s[KT / 32][32];
+                for (int c = 0; c < kChunks; ++c) ld32(s_at + 32 * c, s[0][c]);
 #pragma unroll
-                for (int c = 0; c < KT / 32; ++c) ld32(s_at + 32 * c, s[c]);
+                for (int half = 0; half < 2; ++half) {
+                    const float2 *v = sc + half * kHalfBlocks;
+                    uint32_t (&sh)[kChunks][32] = s[half];
+                    if (half == 1) {
 #pragma unroll
-                for (int c = 0; c < KT / 32; ++c) ld_wait(s[c]);
-                if (!whole) {
-#pragma unroll
-                    for (int i = 0; i < KT; ++i)
-                        if (i > last || i <= first) s[i / 32][i % 32] = 0xFF800000u;  // -inf
-                }
-                float mt = -INFINITY;
-#pragma unroll
-                for (int b = 0; b < P::kBlocks; ++b) {
-                    const uint32_t *x = &s[b / 2][16 * (b & 1)];
-                    float top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-#pragma unroll
-                    for (int i = 2; i < 16; i += 2)
-                        top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-                    v[b].x = factor(v[b].x);
-                    mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
-                }
-                if (__any_sync(0xffffffffu, mt > m + kGrow)) {
-                    const float mn = mt > m + kGrow ? mt : m;
-                    const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
-                    m = mn;
-                    l *= f;
-                    if (j > 0) {
-                        if (!pair) {
-                            // the product of the step before still adds to O
-                            ok = __all_sync(0xffffffffu, wait(pv_done, j - 1));
-                            if (!ok) break;
-                            fence_after();
-                        }
-                        rescale(o_at, f);
+                        for (int c = 0; c < kChunks; ++c) ld32(s_at + kHalf + 32 * c, sh[c]);
                     }
-                }
-                const float ms = m == -INFINITY ? 0.0f : m;
 #pragma unroll
-                for (int b = 0; b < P::kBlocks; ++b) {
-                    const uint32_t *x = &s[b / 2][16 * (b & 1)];
-                    const float add = v[b].y - ms;
-                    const uint64_t ff = two(v[b].x, v[b].x), aa = two(add, add);
-                    uint64_t part = two(0.0f, 0.0f);
-                    uint32_t p[8];  // takes the place of S in TMEM, two values a column
-#pragma unroll
-                    for (int i = 0; i < 16; i += 2) {
-                        const float2 y = untwo(fma2(two(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), ff, aa));
-                        const float e0 = ex2(y.x), e1 = ex2(y.y);
-                        part = add2(part, two(e0, e1));
-                        p[i / 2] = Half2Of<__half>::pack(e0, e1);
-                    }
-                    const float2 t = untwo(part);
-                    l = fmaf(t.x + t.y, ex2(-v[b].y), l);
-                    st8(s_at + 8 * b, p);
-                }
-                } else {
-                // Two times 32 columns in registers, each refilled as soon as it is used, in a loop
-                // that stays small: unrolled over the step, this role and the converting ones
-                // outgrow the instruction cache (measured: a third of all stalls).
-                uint32_t s0[32], s1[32];
-                bool stop = false;
-                auto columns = [&](uint32_t (&s)[32], int c) {
+                    for (int c = 0; c < kChunks; ++c) ld_wait(sh[c]);
                     if (!whole) {
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (32 * c + i > last || 32 * c + i <= first) s[i] = 0xFF800000u;  // -inf
+                        for (int i = 0; i < kHalf; ++i)
+                            if (half * kHalf + i > last || half * kHalf + i <= first) sh[i / 32][i % 32] = 0xFF800000u;  // -inf
                     }
-                    const float2 va = sc[2 * c], vb = sc[2 * c + 1];
-                    const float fa = factor(va.x), fb = factor(vb.x);
-                    float ta = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
-                    float tb = fmaxf(__uint_as_float(s[16]), __uint_as_float(s[17]));
+                    float sum;
+                    while (true) {
+                        const float ms = m == -INFINITY ? 0.0f : m;
+                        float mt = -INFINITY;
+                        sum = 0.0f;
 #pragma unroll
-                    for (int i = 2; i < 16; i += 2) {
-                        ta = fmaxf(fmaxf(ta, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
-                        tb = fmaxf(fmaxf(tb, __uint_as_float(s[16 + i])), __uint_as_float(s[17 + i]));
-                    }
-                    const float mt = fmaxf(fmaf(ta, fa, va.y), fmaf(tb, fb, vb.y));
-                    if (__any_sync(0xffffffffu, mt > m + kGrow)) {
-                        // a new reference, a whole power of two away: l, this step's P so far and O follow
-                        const float mn = mt > m + kGrow ? (m == -INFINITY ? mt : m + ceilf(mt - m)) : m;
+                        for (int b = 0; b < kHalfBlocks; ++b) {
+                            const uint32_t *x = &sh[b / 2][16 * (b & 1)];
+                            const float add = v[b].y - ms;
+                            const uint64_t ff = two(v[b].x, v[b].x), aa = two(add, add);
+                            uint64_t part = two(0.0f, 0.0f);
+                            float top = -INFINITY;
+                            uint32_t p[8];
+#pragma unroll
+                            for (int i = 0; i < 16; i += 2) {
+                                const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
+                                const float2 y = untwo(fma2(two(x0, x1), ff, aa));
+                                const float e0 = ex2(y.x), e1 = ex2(y.y);
+                                top = fmaxf(fmaxf(top, x0), x1);
+                                part = add2(part, two(e0, e1));
+                                p[i / 2] = Half2Of<__half>::pack(e0, e1);
+                            }
+                            mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
+                            const float2 t = untwo(part);
+                            sum = fmaf(t.x + t.y, ex2(-v[b].y), sum);
+                            st8(s_at + half * (kHalf / 2) + 8 * b, p);
+                        }
+                        if (!__any_sync(0xffffffffu, mt > m + kGrow)) break;
+                        const float mn = mt > m + kGrow ? mt : m;
                         const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
                         m = mn;
                         l *= f;
-                        st_wait();
-#pragma unroll 1
-                        for (int k = 0; k < c; ++k) {
-                            uint32_t p[16];
-                            ld16(s_at + 16 * k, p);
-                            ld_wait(p);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) {
-                                const float2 v = Half2Of<__half>::f2(p[i]);  // f itself may be below fp16's range
-                                p[i] = Half2Of<__half>::pack(v.x * f, v.y * f);
-                            }
-                            st16(s_at + 16 * k, p);
-                        }
-                        if (j > 0 && !pair && !stop) {
-                            // the product of the step before still adds to O
-                            stop = !__all_sync(0xffffffffu, wait(pv_done, j - 1));
+                        if (j > 0 || half) {
+                            // what still adds to O: the first half's product, or with one tile
+                            // that of the step before (with two it is done before S comes)
+                            if (!pair && j > 0) ok = wait(pv_done, j - 1);
+                            if (ok && half) ok = wait(pv_half(w), j);
+                            ok = __all_sync(0xffffffffu, ok);
+                            if (!ok) break;
                             fence_after();
-                        }
-                        if (j > 0 && !stop) rescale(o_at, f);
-                    }
-                    const float ms = m == -INFINITY ? 0.0f : m;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t p[8];  // takes the place of S in TMEM, two values a column
-                        const float f = h ? fb : fa, lv = h ? vb.y : va.y, add = lv - ms;
-                        const uint64_t ff = two(f, f), aa = two(add, add);
-                        uint64_t part = two(0.0f, 0.0f);
-#pragma unroll
-                        for (int i = 0; i < 16; i += 2) {
-                            const float2 x = untwo(fma2(two(__uint_as_float(s[16 * h + i]),
-                                                            __uint_as_float(s[16 * h + i + 1])), ff, aa));
-                            const float e0 = ex2(x.x), e1 = ex2(x.y);
-                            part = add2(part, two(e0, e1));
-                            p[i / 2] = Half2Of<__half>::pack(e0, e1);
-                        }
-                        const float2 t = untwo(part);
-                        l = fmaf(t.x + t.y, ex2(-lv), l);
-                        st8(s_at + 16 * c + 8 * h, p);
-                    }
-                };
-                constexpr int kChunks = KT / 32;
-                ld32(s_at, s0);
-                ld32(s_at + 32, s1);
 #pragma unroll 1
-                for (int c = 0; c < kChunks; c += 2) {
-                    ld_wait(s0);
-                    ld_wait(s1);
-                    columns(s0, c);
-                    if (c + 2 < kChunks) ld32(s_at + 32 * (c + 2), s0);
-                    columns(s1, c + 1);
-                    if (c + 2 < kChunks) ld32(s_at + 32 * (c + 3), s1);
+                            for (int k = 0; k < D / 16; ++k) {
+                                uint32_t o[16];
+                                ld16(o_at + 16 * k, o);
+                                ld_wait(o);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                                st16(o_at + 16 * k, o);
+                            }
+                        }
+                    }
+                    if (!ok) break;
+                    l += sum;
+                    st_wait();
+                    fence_before();
+                    mbar_arrive(p_full(slot, half));
                 }
-                if (stop) { ok = false; break; }
-                }
-                st_wait();
-                fence_before();
-                mbar_arrive(p_full(slot));
+                if (!ok) break;
             }
             // ---- out --------------------------------------------------------------
             if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(o_full(w), 0));
@@ -555,30 +504,35 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wa
         };
         if constexpr (STAGED) {
             // ---- copies of staged tiles -------------------------------------------------
-            if (lane == 0) {
-                const int64_t first = ((int64_t)row * a.L.heads + head) * st.steps + (k_lo - all_steps.lo) / KT;
-                int j = 0, v_issued = 0;
-                for (; j < steps; ++j) {
-                    const uint8_t *tile = st.tiles + (first + j) * (2 * P::kKV);
-                    if (j >= kStages && !wait(k_empty(j), j / kStages - 1)) break;
+            // one box a panel: KT rows of 128 bytes
+            const int64_t first = ((int64_t)row * a.L.heads + head) * st.steps + (k_lo - all_steps.lo) / KT;
+            auto copy = [&](uint32_t to, int64_t tile, uint32_t full) {
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(full, P::kKV);
+                    for (int p = 0; p < P::kPanels; ++p)
+                        tma_load_2d(to + p * P::kPanelKV, &map, 0, (int)((tile * P::kPanels + p) * KT), full);
+                }
+            };
+            int j = 0, v_issued = 0;
+            for (; j < steps; ++j) {
+                if (j >= kStages && !__all_sync(0xffffffffu, wait(k_empty(j), j / kStages - 1))) break;
+                if (lane == 0) {
                     mbar_arrive_expect_tx(sc_full(j), P::kBlocks * 8);
                     bulk_g2s(smem_addr(scales[j % kScaleRing]), st.scales + (first + j) * P::kBlocks, P::kBlocks * 8, sc_full(j));
-                    mbar_arrive_expect_tx(k_full(j), P::kKV);
-                    bulk_g2s(base + P::kOffK + (j % kStages) * P::kKV, tile, P::kKV, k_full(j));
-                    if (j >= kStages && !wait(v_empty(j), j / kStages - 1)) {
-                        ++j;
-                        break;
-                    }
-                    mbar_arrive_expect_tx(v_full(j), P::kKV);
-                    bulk_g2s(base + P::kOffV + (j % kStages) * P::kKV, tile + P::kKV, P::kKV, v_full(j));
-                    v_issued = j + 1;
                 }
-                // nothing of this CTA's is in flight when it leaves
-                for (int i = max(0, j - kStages); i < j; ++i) {
-                    mbar_wait_for(k_full(i), (i / kStages) & 1, kDrainWaitNs, &g_prefill_timeouts);
-                    if (i < v_issued) mbar_wait_for(v_full(i), (i / kStages) & 1, kDrainWaitNs, &g_prefill_timeouts);
-                    mbar_wait_for(sc_full(i), (i / kScaleRing) & 1, kDrainWaitNs, &g_prefill_timeouts);
+                copy(base + P::kOffK + (j % kStages) * P::kKV, 2 * (first + j), k_full(j));
+                if (j >= kStages && !__all_sync(0xffffffffu, wait(v_empty(j), j / kStages - 1))) {
+                    ++j;
+                    break;
                 }
+                copy(base + P::kOffV + (j % kStages) * P::kKV, 2 * (first + j) + 1, v_full(j));
+                v_issued = j + 1;
+            }
+            // nothing of this CTA's is in flight when it leaves
+            for (int i = max(0, j - kStages); i < j; ++i) {
+                mbar_wait_for(k_full(i), (i / kStages) & 1, kDrainWaitNs, &g_prefill_timeouts);
+                if (i < v_issued) mbar_wait_for(v_full(i), (i / kStages) & 1, kDrainWaitNs, &g_prefill_timeouts);
+                mbar_wait_for(sc_full(i), (i / kScaleRing) & 1, kDrainWaitNs, &g_prefill_timeouts);
             }
         } else if (steps > 0) {
             if (warp < kMmaWarp)
@@ -599,24 +553,36 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wa
                        k + ((s / 4) * P::kPanelKV + (s % 4) * 32) / 16, hi_word, i_qk, s > 0);
             commit(s_full(slot));
         };
-        auto pv = [&](int j, int w, int slot) {
+        auto pv = [&](int j, int w, int slot, int half) {
             const uint32_t v = v_lo + (j % kStages) * (P::kKV / 16);
 #pragma unroll
-            for (int s = 0; s < KT / 16; ++s)
+            for (int i = 0; i < KT / 32; ++i) {
+                const int s = half * (KT / 32) + i;
                 mma_ts(tmem + (w ? P::kO1 : P::kO0), tmem + (slot ? P::kS1 : 0) + 8 * s, v + s * (16 * 128 / 16), hi_word,
                        i_pv, j > 0 || s > 0);
+            }
+            if (!half) commit(pv_half(w));
         };
-        // The tiles are written by ordinary stores and read by the MMAs: the fence between the two
-        // stands here, after the wait, because the writers have loads in flight that a fence of
-        // theirs would wait for.
+        // What ordinary stores wrote (Q, and the tiles of the direct form) is read by the MMAs: the
+        // fence between the two stands here, after the wait, because the writers have loads in
+        // flight that a fence of theirs would wait for.  Bulk copies need none.
         auto filled = [&] {
             fence_after();
-            fence_proxy_async_smem();
+            if (!STAGED) fence_proxy_async_smem();
         };
         auto all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
+        auto both = [&](int j, int w, int slot, int parity) {  // O += P V of a step, by halves
+            for (int half = 0; half < 2; ++half) {
+                if (!all(p_full(slot, half), parity)) return false;
+                fence_after();
+                pv(j, w, slot, half);
+            }
+            return true;
+        };
         bool ok = steps > 0 && all(q_full, 0) && all(k_full(0), 0);
         if (ok) {
             filled();
+            fence_proxy_async_smem();
             qk(0, 0, 0);
             if (pair) qk(0, 1, 1);
             commit(k_empty(0));
@@ -630,16 +596,12 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wa
             if (!ok) break;
             filled();
             if (pair) {
-                ok = all(p_full(0), j);
+                ok = both(j, 0, 0, j);
                 if (!ok) break;
-                fence_after();
-                pv(j, 0, 0);
                 if (next) qk(j + 1, 0, 0);
                 else commit(o_full(0));
-                ok = all(p_full(1), j);
+                ok = both(j, 1, 1, j);
                 if (!ok) break;
-                fence_after();
-                pv(j, 1, 1);
                 commit(v_empty(j));
                 if (next) {
                     qk(j + 1, 1, 1);
@@ -655,10 +617,8 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, unsigned long long wa
                 ok = all(v_full(j), j / kStages);
                 if (!ok) break;
                 filled();
-                ok = all(p_full(j & 1), j >> 1);
+                ok = both(j, 0, j & 1, j >> 1);
                 if (!ok) break;
-                fence_after();
-                pv(j, 0, j & 1);
                 commit(v_empty(j));
                 commit(pv_done);
                 if (!next) commit(o_full(0));
@@ -738,6 +698,21 @@ bool configure(K kern, size_t smem, bool (&done)[64])
     return true;
 }
 
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(ptr);
+    });
+    return fn;
+}
+
 // Steps of a row that the scratch is laid out for, and its bytes
 template <int D>
 int staged_steps(const AttendArgs &a)
@@ -762,17 +737,26 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
     const int64_t rows = (int64_t)a.max_new * a.group;
     const dim3 grid((unsigned)((rows + P::kRows - 1) / P::kRows), (unsigned)a.L.heads, (unsigned)a.L.rows);
     Staged st = {nullptr, nullptr, 0};
+    CUtensorMap map = {};
     if (a.work) {
         st.steps = staged_steps<D>(a);
         const int64_t tiles = (int64_t)a.L.rows * a.L.heads * st.steps;
         st.tiles = static_cast<uint8_t *>(a.work);
         st.scales = reinterpret_cast<float2 *>(st.tiles + tiles * 2 * P::kKV);
+        // the scratch as rows of 64 fp16, already in the swizzled order of the operands
+        auto enc = encode_fn();
+        const cuuint64_t dims[2] = {64, (cuuint64_t)(tiles * 2 * P::kPanels * P::KT)}, strides[1] = {128};
+        const cuuint32_t box[2] = {64, (cuuint32_t)P::KT}, each[2] = {1, 1};
+        if (!enc || enc(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, st.tiles, dims, strides, box, each,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return BQD_ERR_CUDA;
         stage_kernel<D, FMT><<<dim3(2 * st.steps, a.L.heads, a.L.rows), 256, 0, s>>>(a, st);
-        staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, opt_wait_ns());
+        staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, map, opt_wait_ns());
         // a row can only be longer than planned where the plan is below the table's capacity
         if ((int64_t)a.max_len >= ((int64_t)a.L.row_pages << a.L.page_shift)) return cuda_status(cudaGetLastError());
     }
-    direct<<<grid, kThreadsF, P::kSmem, s>>>(a, st, opt_wait_ns());
+    direct<<<grid, kThreadsF, P::kSmem, s>>>(a, st, map, opt_wait_ns());
     return cuda_status(cudaGetLastError());
 }
 
