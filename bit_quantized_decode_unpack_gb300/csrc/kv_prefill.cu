@@ -165,10 +165,12 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int head = blockIdx.y, row = blockIdx.z;
+    // query tiles in the slowest place of the grid, the last first: those see most keys, and
+    // what starts last is short
+    const int head = blockIdx.x, row = blockIdx.y;
     const Span span(a.starts, row, a.tokens, a.max_new);
     const int rows = span.n * a.group;
-    const int r0 = (int)(gridDim.x - 1 - blockIdx.x) * P::kRows;  // the last queries see most keys: first
+    const int r0 = (int)(gridDim.z - 1 - blockIdx.z) * P::kRows;
     if (r0 >= rows) return;
     const int L = a.L.length(row);
     const RowSteps all_steps(L, span.n, a.window, KT);
@@ -735,7 +737,9 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
     static bool done[2][64] = {};
     if (!configure(direct, P::kSmem, done[0]) || !configure(staged, P::kSmem, done[1])) return BQD_ERR_CUDA;
     const int64_t rows = (int64_t)a.max_new * a.group;
-    const dim3 grid((unsigned)((rows + P::kRows - 1) / P::kRows), (unsigned)a.L.heads, (unsigned)a.L.rows);
+    const int64_t q_tiles = (rows + P::kRows - 1) / P::kRows;
+    if (q_tiles > 65535) return BQD_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)a.L.heads, (unsigned)a.L.rows, (unsigned)q_tiles);
     Staged st = {nullptr, nullptr, 0};
     CUtensorMap map = {};
     if (a.work) {
