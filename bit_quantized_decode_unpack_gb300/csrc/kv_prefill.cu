@@ -506,13 +506,12 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant
         };
         if constexpr (STAGED) {
             // ---- copies of staged tiles -------------------------------------------------
-            // one box a panel: KT rows of 128 bytes
+            // a tile is one box of 128 or 256 rows of 128 bytes
             const int64_t first = ((int64_t)row * a.L.heads + head) * st.steps + (k_lo - all_steps.lo) / KT;
             auto copy = [&](uint32_t to, int64_t tile, uint32_t full) {
                 if (lane == 0) {
                     mbar_arrive_expect_tx(full, P::kKV);
-                    for (int p = 0; p < P::kPanels; ++p)
-                        tma_load_2d(to + p * P::kPanelKV, &map, 0, (int)((tile * P::kPanels + p) * KT), full);
+                    tma_load_2d(to, &map, 0, (int)(tile * (P::kPanels * KT)), full);
                 }
             };
             int j = 0, v_issued = 0;
@@ -750,15 +749,16 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
         // the scratch as rows of 64 fp16, already in the swizzled order of the operands
         auto enc = encode_fn();
         const cuuint64_t dims[2] = {64, (cuuint64_t)(tiles * 2 * P::kPanels * P::KT)}, strides[1] = {128};
-        const cuuint32_t box[2] = {64, (cuuint32_t)P::KT}, each[2] = {1, 1};
+        const cuuint32_t box[2] = {64, (cuuint32_t)(P::kPanels * P::KT)}, each[2] = {1, 1};
         if (!enc || enc(&map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, st.tiles, dims, strides, box, each,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return BQD_ERR_CUDA;
         stage_kernel<D, FMT><<<dim3(2 * st.steps, a.L.heads, a.L.rows), 256, 0, s>>>(a, st);
         staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, map, opt_wait_ns());
-        // a row can only be longer than planned where the plan is below the table's capacity
-        if ((int64_t)a.max_len >= ((int64_t)a.L.row_pages << a.L.page_shift)) return cuda_status(cudaGetLastError());
+        // a row can only need more steps than planned where the table's capacity does
+        const int64_t capacity = (int64_t)a.L.row_pages << a.L.page_shift;
+        if ((int64_t)st.steps * P::KT >= capacity) return cuda_status(cudaGetLastError());
     }
     direct<<<grid, kThreadsF, P::kSmem, s>>>(a, st, map, opt_wait_ns());
     return cuda_status(cudaGetLastError());
