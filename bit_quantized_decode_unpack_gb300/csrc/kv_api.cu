@@ -91,9 +91,10 @@ int planned_length(const bqd_kv_cache &c, int64_t max_len)
 // queries enough for tiles of 128 (query, head) rows on the tensor cores
 bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group >= 64; }
 
-// bytes of scratch that a call of many queries is better with, or 0
-int64_t staged_need(const AttendArgs &a)
+// bytes of scratch that a call is better with, or 0
+int64_t scratch_need(const AttendArgs &a)
 {
+    if (!many_queries(a)) return decode_workspace(a);
     const int64_t bytes = prefill_workspace(a);
     return bytes <= kMaxStaged ? bytes : 0;
 }
@@ -142,7 +143,8 @@ extern "C" int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_head
     a.group = q_heads / c.kv_heads;
     a.max_new = (int)max_new;
     a.max_len = planned_length(c, max_len);
-    return many_queries(a) ? staged_need(a) : 0;
+    a.window = 0;
+    return scratch_need(a);
 }
 
 extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride,
@@ -179,10 +181,9 @@ extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q
     a.window = (int)(window < most ? window : 0);  // one past any position hides nothing
     a.q_vec = vec_ok(q, q_token_stride, q_head_stride);
     a.work = nullptr;
-    if (!many_queries(a)) return launch_attend_decode(a, to_stream(stream));
-    const int64_t need = staged_need(a);
+    const int64_t need = scratch_need(a);
     if (need > 0 && work_bytes >= need) a.work = work;
-    return launch_attend_prefill(a, to_stream(stream));
+    return many_queries(a) ? launch_attend_prefill(a, to_stream(stream)) : launch_attend_decode(a, to_stream(stream));
 }
 
 extern "C" int bqd_kv_reserve(const bqd_kv_cache *cache, const int32_t *counts, int32_t *base, int32_t *copies,

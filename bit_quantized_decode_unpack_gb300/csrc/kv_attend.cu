@@ -24,10 +24,20 @@
 // a tile (32 D bytes) is always in flight for each warp.
 // Codes are exact in fp16 and q is scaled by a power of two into its range.
 //
-// The keys of one (row, KV head, column tile) are split over the 8 warps of a
-// CTA and the S CTAs of a cluster; partial (m, l, O) are joined through shared
-// and distributed shared memory in a fixed order: one launch, no scratch, the
-// same bits every time.
+// Work.  A unit is (row, KV head, column tile of 8 NT queries); its key tiles are
+// interleaved over the warps of a CTA, whose partial (m, l, O) are joined through
+// shared memory.  Units are spread over the GPU in one of two ways:
+//   shares   the tiles of all units, laid end to end, are cut into equal shares,
+//            one for each CTA that can be resident (no launch knows the rows'
+//            lengths: each CTA adds them up).  What a share cuts off a unit goes
+//            to scratch, and a second kernel, launched early, joins the pieces
+//            in order.  Lengths of any mix load the GPU evenly: 32 sequences of 0
+//            to 8191 tokens 58 us with clusters, 45 us with shares.
+//   cluster  the CTAs of a cluster split a unit's keys and join through
+//            distributed shared memory: one launch, no scratch.  For calls whose
+//            few keys would not fill the shares (latency counts), for batches of
+//            more rows than a CTA adds up, and where there is no scratch.
+// Both are free of atomics, and give the same bits every time.
 #include <algorithm>
 #include <cmath>
 
@@ -40,8 +50,11 @@ namespace {
 
 using namespace qmvdev;
 
-constexpr int kWarpsD = 8;
-constexpr int kMaxSplit = 16;  // CTAs of a cluster
+constexpr int kMaxSplit = 8;      // CTAs of a cluster (16 are placed badly: 130001 tokens, 227 us against 165)
+constexpr int kMaxPlanRows = 1024; // rows that a CTA adds up
+constexpr int kMinShare = 32;     // tiles of a share at least
+constexpr int kUnitCost = 24;     // what a unit costs beside its tiles (q, the first loads, the join), in tiles:
+                                  // 32 mixed sequences 81 us with 0, 58 with 8, 45 with 24, 47 with 48
 constexpr float kGrow = 8.0f;  // a reference m is replaced when x passes it by this much
 
 __device__ __forceinline__ float ex2(float x)
@@ -79,45 +92,141 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t local_addr, uint32_t
     return v;
 }
 
+// Warps and resident CTAs follow the registers: K and V words, O and q take
+// D / 4 + 8 NT (D / 16) + ...: 128 a thread for 8 columns of D <= 128.
 template <int D, int NT>
 struct Tile {
+    static constexpr int kWarps = NT > 1 ? 4 : 8;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kResident = D == 256 ? 1 : NT > 1 ? 3 : 2;  // CTAs of an SM
     static constexpr int kCols = 8 * NT;
     static constexpr int kPitch = D + 4;  // floats of a column in shared memory
     // floats: per-warp partials, then the CTA's joined partial and its m, l
     static constexpr int kWarpFloats = kCols * kPitch;
-    static constexpr size_t kSmem = sizeof(float) * ((size_t)kWarpsD * kWarpFloats + 2 * kWarpsD * kCols +
-                                                     (size_t)kWarpFloats + 2 * kCols);
+    static constexpr size_t kFloats = (size_t)kWarps * kWarpFloats + 2 * kWarps * kCols + (size_t)kWarpFloats + 2 * kCols;
+    static constexpr size_t kSmem = sizeof(float) * kFloats;
+    // scratch of a piece: O [cols][D], m [cols], l [cols]
+    static constexpr int kPiece = kCols * D + 2 * kCols;
 };
 
-template <typename T, int D, int FMT, int NT>
-__global__ void __launch_bounds__(kWarpsD * 32, (D == 256 || NT > 1) ? 1 : 2)
-attend_decode_kernel(const AttendArgs a, int S)
+// The first piece of a unit that goes on in later shares
+struct Cut {
+    int row, head, ctile, last;  // last: the share with its last piece; row < 0: none
+};
+
+struct Shares {
+    float *pieces;  // [shares][2][kPiece]: what began earlier, what goes on
+    Cut *cuts;      // [shares]
+    int count;      // 0: clusters
+};
+
+// What the queries of a column tile see
+struct View {
+    Span span;
+    int L, cols, c0, p_min, p_max, lo, hi;
+    __device__ __forceinline__ View(const AttendArgs &a, int row, int ctile, int kCols)
+        : span(a.starts, row, a.tokens, a.max_new)
+    {
+        L = a.L.length(row);
+        cols = span.n * a.group;  // columns: query-major, then head of the group
+        c0 = ctile * kCols;
+        const int i_min = c0 / a.group, i_max = (min(c0 + kCols, cols) - 1) / a.group;
+        p_min = L - span.n + i_min;
+        p_max = L - span.n + i_max;
+        hi = max(0, p_max + 1);
+        lo = a.window > 0 ? max(0, p_min + 1 - a.window) : 0;
+    }
+};
+
+// Tiles of a row that any of its queries sees: [lo, lo + n) (n >= 1: a row that
+// sees nothing has one, so that its zeros are written)
+struct RowTiles {
+    int lo, n, ctiles;
+    __device__ __forceinline__ RowTiles(const AttendArgs &a, int row, int kCols)
+    {
+        const Span span(a.starts, row, a.tokens, a.max_new);
+        const int L = a.L.length(row);
+        lo = a.window > 0 ? max(0, L - span.n + 1 - a.window) >> 4 : 0;
+        n = max(1, ((L + 15) >> 4) - lo);
+        ctiles = (span.n * a.group + kCols - 1) / kCols;
+    }
+};
+
+template <typename T, int D>
+__device__ __forceinline__ void finish(const AttendArgs &a, const View &v, int head, int col, int d, float4 o, float mm,
+                                       float ll)
+{
+    using H = Half2Of<T>;
+    const int c = v.c0 + col;
+    if (c >= v.cols) return;
+    const int token = v.span.lo + c / a.group, hq = head * a.group + c % a.group;
+    const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
+    T *at = static_cast<T *>(a.out) + ((int64_t)token * a.q_heads + hq) * D + d;
+    *reinterpret_cast<uint2 *>(at) = make_uint2(H::pack(o.x * r, o.y * r), H::pack(o.z * r, o.w * r));
+    if (a.lse && d == 0)
+        a.lse[(int64_t)token * a.q_heads + hq] = ll == 0.0f ? -INFINITY : 0.69314718055994531f * (mm + log2f(ll));
+}
+
+// Columns of a unit against its tiles [j0, j1): each warp takes every kWarps-th.
+// The joined (o, m, l) of each quad of dims goes to emit(col, d, o, m, l).
+template <typename T, int D, int FMT, int NT, typename Emit>
+__device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_, int row, int head, int j0, int j1,
+                                           float *smem, Emit emit)
 {
     using C = Code<FMT>;
     using H = Half2Of<T>;
     using TL = Tile<D, NT>;
+    constexpr int kWarpsD = TL::kWarps;
     constexpr int KW = D / 16;   // 32-bit words of a lane's part of one K row
     constexpr int VW = D / 32;   // words of a lane's part of one V token
     constexpr int KS = D / 16;   // k16 steps of S, m16 tiles of O^T
-    extern __shared__ __align__(16) float smem[];
-
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, t = lane & 3;
-    const int rank = S > 1 ? (int)cluster_ctarank() : 0;
-    const int ctile = blockIdx.x / S, head = blockIdx.y, row = blockIdx.z;
-    const Span span(a.starts, row, a.tokens, a.max_new);
-    const int cols = span.n * a.group;       // columns: query-major, then head of the group
-    const int c0 = ctile * TL::kCols;
-    if (c0 >= cols) return;                  // the whole cluster leaves
-    const int L = a.L.length(row);
-    const int i_min = c0 / a.group, i_max = (min(c0 + TL::kCols, cols) - 1) / a.group;
-    const int p_min = L - span.n + i_min, p_max = L - span.n + i_max;
-    const int hi = max(0, p_max + 1);
-    const int lo = a.window > 0 ? max(0, p_min + 1 - a.window) : 0;
-    // this CTA's tiles [j0, j1) of 16 tokens
-    const int tile_lo = lo >> 4, tiles = max(0, ((hi + 15) >> 4) - tile_lo);
-    const int j0 = tile_lo + (int)((int64_t)tiles * rank / S), j1 = tile_lo + (int)((int64_t)tiles * (rank + 1) / S);
+    const Span &span = vw_.span;
+    const int cols = vw_.cols, c0 = vw_.c0, L = vw_.L, p_min = vw_.p_min, p_max = vw_.p_max;
 
+    // the first tile is on its way while q is prepared
+    uint32_t kw[2][KW], vw[4][VW];
+    float ksc = 0.0f, vsc = 1.0f;
+    auto load_k = [&](int64_t blk) {
+        const uint8_t *at = a.L.k + blk * (kBlock * D) + 16 * t;
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int j = 0; j < D / 64; ++j) {
+                const uint4 v = ld_stream_v4(at + (g + 8 * r) * D + 64 * j);
+                kw[r][4 * j] = v.x, kw[r][4 * j + 1] = v.y, kw[r][4 * j + 2] = v.z, kw[r][4 * j + 3] = v.w;
+            }
+        ksc = __ldg(a.L.ks + blk);
+    };
+    auto load_v = [&](int64_t blk) {
+        const uint8_t *at = a.L.v + blk * (kBlock * D);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const uint8_t *tok = at + (2 * t + (r & 1) + 8 * (r >> 1)) * D;
+            if constexpr (D == 64) {
+                const uint2 v = ld_stream_v2(tok + 8 * g);
+                vw[r][0] = v.x, vw[r][1] = v.y;
+            } else {
+#pragma unroll
+                for (int j = 0; j < D / 128; ++j) {
+                    const uint4 v = ld_stream_v4(tok + 16 * (g + 8 * j));
+                    vw[r][4 * j] = v.x, vw[r][4 * j + 1] = v.y, vw[r][4 * j + 2] = v.z, vw[r][4 * j + 3] = v.w;
+                }
+            }
+        }
+        vsc = __ldg(a.L.vs + blk);
+    };
+
+    int j = j0 + warp;
+    int64_t blk = 0;
+    int next_page = 0;  // as listed, of the tile after the next
+    if (j < j1) {
+        blk = a.L.block_of(row, head, j << 4);
+        load_k(blk);
+        load_v(blk);
+        if (j + kWarpsD < j1) next_page = a.L.listed(row, (j + kWarpsD) << 4);
+    }
     // q: column n*8 + g, the dims of this lane's K chunks, scaled by 2^-e
     uint32_t qf[NT][KS][2];
     float cs[NT][2];             // f 2^e of columns n*8 + 2t, + 2t + 1
@@ -185,47 +294,6 @@ attend_decode_kernel(const AttendArgs a, int S)
         for (int k = 0; k < KS; ++k) acc[n][k][0] = acc[n][k][1] = acc[n][k][2] = acc[n][k][3] = 0.0f;
     }
 
-    uint32_t kw[2][KW], vw[4][VW];
-    float ksc = 0.0f, vsc = 1.0f;
-    auto load_k = [&](int64_t blk) {
-        const uint8_t *at = a.L.k + blk * (kBlock * D) + 16 * t;
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int j = 0; j < D / 64; ++j) {
-                const uint4 v = ld_stream_v4(at + (g + 8 * r) * D + 64 * j);
-                kw[r][4 * j] = v.x, kw[r][4 * j + 1] = v.y, kw[r][4 * j + 2] = v.z, kw[r][4 * j + 3] = v.w;
-            }
-        ksc = __ldg(a.L.ks + blk);
-    };
-    auto load_v = [&](int64_t blk) {
-        const uint8_t *at = a.L.v + blk * (kBlock * D);
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const uint8_t *tok = at + (2 * t + (r & 1) + 8 * (r >> 1)) * D;
-            if constexpr (D == 64) {
-                const uint2 v = ld_stream_v2(tok + 8 * g);
-                vw[r][0] = v.x, vw[r][1] = v.y;
-            } else {
-#pragma unroll
-                for (int j = 0; j < D / 128; ++j) {
-                    const uint4 v = ld_stream_v4(tok + 16 * (g + 8 * j));
-                    vw[r][4 * j] = v.x, vw[r][4 * j + 1] = v.y, vw[r][4 * j + 2] = v.z, vw[r][4 * j + 3] = v.w;
-                }
-            }
-        }
-        vsc = __ldg(a.L.vs + blk);
-    };
-
-    int j = j0 + warp;
-    int64_t blk = 0;
-    int next_page = 0;  // as listed, of the tile after the next
-    if (j < j1) {
-        blk = a.L.block_of(row, head, j << 4);
-        load_k(blk);
-        load_v(blk);
-        if (j + kWarpsD < j1) next_page = a.L.listed(row, (j + kWarpsD) << 4);
-    }
     for (; j < j1; j += kWarpsD) {
         const int t0 = j << 4;
         const bool more = j + kWarpsD < j1;
@@ -323,8 +391,6 @@ attend_decode_kernel(const AttendArgs a, int S)
     float *part = smem;                                  // [warp][col][kPitch]
     float *wm = part + kWarpsD * TL::kWarpFloats;        // [warp][col]
     float *wl = wm + kWarpsD * TL::kCols;
-    float *joined = wl + kWarpsD * TL::kCols;            // [col][kPitch]
-    float *jm = joined + TL::kWarpFloats, *jl = jm + TL::kCols;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -348,17 +414,6 @@ attend_decode_kernel(const AttendArgs a, int S)
         }
     }
     __syncthreads();
-    auto finish = [&](int col, int d, float4 o, float mm, float ll) {
-        const int c = c0 + col;
-        if (c >= cols) return;
-        const int token = span.lo + c / a.group, hq = head * a.group + c % a.group;
-        const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
-        T *at = static_cast<T *>(a.out) + ((int64_t)token * a.q_heads + hq) * D + d;
-        *reinterpret_cast<uint2 *>(at) = make_uint2(H::pack(o.x * r, o.y * r), H::pack(o.z * r, o.w * r));
-        if (a.lse && d == 0)
-            a.lse[(int64_t)token * a.q_heads + hq] =
-                ll == 0.0f ? -INFINITY : 0.69314718055994531f * (mm + log2f(ll));
-    };
     constexpr int kQuads = TL::kCols * D / 4;
     for (int i = threadIdx.x; i < kQuads; i += kWarpsD * 32) {
         const int col = i / (D / 4), d = (i % (D / 4)) * 4;
@@ -375,17 +430,39 @@ attend_decode_kernel(const AttendArgs a, int S)
             o.x = fmaf(v.x, r, o.x), o.y = fmaf(v.y, r, o.y), o.z = fmaf(v.z, r, o.z), o.w = fmaf(v.w, r, o.w);
             ll = fmaf(wl[w * TL::kCols + col], r, ll);
         }
+        emit(col, d, o, mm, ll);
+    }
+    __syncthreads();  // the partials' place may be written again
+}
+
+template <typename T, int D, int FMT, int NT>
+__global__ void __launch_bounds__(Tile<D, NT>::kThreads, Tile<D, NT>::kResident)
+attend_cluster_kernel(const AttendArgs a, int S)
+{
+    using TL = Tile<D, NT>;
+    extern __shared__ __align__(16) float smem[];
+    const int rank = S > 1 ? (int)cluster_ctarank() : 0;
+    const int ctile = blockIdx.x / S, head = blockIdx.y, row = blockIdx.z;
+    const View v(a, row, ctile, TL::kCols);
+    if (v.c0 >= v.cols) return;              // the whole cluster leaves
+    // this CTA's tiles of 16 tokens
+    const int tile_lo = v.lo >> 4, tiles = max(0, ((v.hi + 15) >> 4) - tile_lo);
+    const int j0 = tile_lo + (int)((int64_t)tiles * rank / S), j1 = tile_lo + (int)((int64_t)tiles * (rank + 1) / S);
+    float *joined = smem + TL::kWarps * (TL::kWarpFloats + 2 * TL::kCols);  // [col][kPitch]
+    float *jm = joined + TL::kWarpFloats, *jl = jm + TL::kCols;
+    unit_tiles<T, D, FMT, NT>(a, v, row, head, j0, j1, smem, [&](int col, int d, float4 o, float mm, float ll) {
         if (S == 1) {
-            finish(col, d, o, mm, ll);
+            finish<T, D>(a, v, head, col, d, o, mm, ll);
         } else {
             *reinterpret_cast<float4 *>(joined + col * TL::kPitch + d) = o;
             if (d == 0) jm[col] = mm, jl[col] = ll;
         }
-    }
+    });
     if (S == 1) return;
-    // ---- join the CTAs: rank r finishes the quads r, r + S, ... ------------------
+    // rank r finishes the quads r, r + S, ...
     cluster_sync();
-    for (int i = threadIdx.x * S + rank; i < kQuads; i += kWarpsD * 32 * S) {
+    constexpr int kQuads = TL::kCols * D / 4;
+    for (int i = threadIdx.x * S + rank; i < kQuads; i += TL::kThreads * S) {
         const int col = i / (D / 4), d = (i % (D / 4)) * 4;
         float mm = -INFINITY;
         for (int r = 0; r < S; ++r) mm = fmaxf(mm, ld_cluster_f32(smem_addr(jm + col), r));
@@ -394,13 +471,136 @@ attend_decode_kernel(const AttendArgs a, int S)
         for (int r = 0; r < S; ++r) {
             const float mr = ld_cluster_f32(smem_addr(jm + col), r);
             const float f = mr == -INFINITY ? 0.0f : ex2(mr - mm);
-            const float4 v = ld_cluster_f32x4(smem_addr(joined + col * TL::kPitch + d), r);
-            o.x = fmaf(v.x, f, o.x), o.y = fmaf(v.y, f, o.y), o.z = fmaf(v.z, f, o.z), o.w = fmaf(v.w, f, o.w);
+            const float4 x = ld_cluster_f32x4(smem_addr(joined + col * TL::kPitch + d), r);
+            o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
             ll = fmaf(ld_cluster_f32(smem_addr(jl + col), r), f, ll);
         }
-        finish(col, d, o, mm, ll);
+        finish<T, D>(a, v, head, col, d, o, mm, ll);
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
+}
+
+template <typename T, int D, int FMT, int NT>
+__global__ void __launch_bounds__(Tile<D, NT>::kThreads, Tile<D, NT>::kResident)
+attend_shares_kernel(const AttendArgs a, const Shares sh)
+{
+    using TL = Tile<D, NT>;
+    extern __shared__ __align__(16) float smem[];
+    __shared__ int64_t before[kMaxPlanRows + 1];  // tiles of all units of the rows before
+    __shared__ int64_t warp_sums[TL::kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, share = blockIdx.x;
+    // the rows' tiles and their sums: a thread takes consecutive rows
+    const int rows = a.L.rows, each = (rows + TL::kThreads - 1) / TL::kThreads;
+    int64_t mine = 0;
+    for (int i = 0; i < each; ++i) {
+        const int r = tid * each + i;
+        if (r >= rows) break;
+        const RowTiles rt(a, r, TL::kCols);
+        const int64_t w = (int64_t)(rt.n + kUnitCost) * rt.ctiles * a.L.heads;
+        before[r] = w;
+        mine += w;
+    }
+    int64_t x = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sums[warp] = x;
+    __syncthreads();
+    int64_t total = 0, base = 0;
+    for (int w = 0; w < TL::kWarps; ++w) {
+        if (w == warp) base = total;
+        total += warp_sums[w];
+    }
+    int64_t at = base + x - mine;
+    for (int i = 0; i < each; ++i) {
+        const int r = tid * each + i;
+        if (r >= rows) break;
+        const int64_t w = before[r];
+        before[r] = at;
+        at += w;
+    }
+    if (tid == 0) before[rows] = total;
+    __syncthreads();
+    const int64_t per = max((int64_t)kMinShare, (total + sh.count - 1) / sh.count);
+    int64_t pos = min(total, share * per);
+    const int64_t end = min(total, pos + per);
+    bool cut = false;
+    int row = 0;
+    while (pos < end) {
+        {
+            int lo = row, hi = rows - 1;  // the last row with before <= pos
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (before[mid] <= pos) lo = mid;
+                else hi = mid - 1;
+            }
+            row = lo;
+        }
+        const RowTiles rt(a, row, TL::kCols);
+        const int64_t off = pos - before[row];
+        const int cost = rt.n + kUnitCost;  // the first kUnitCost of a unit stand for no tile
+        const int unit = (int)(off / cost), j = (int)(off - (int64_t)unit * cost);
+        const int head = unit % a.L.heads, ctile = unit / a.L.heads;
+        const int stop = (int)min((int64_t)cost, j + (end - pos));
+        const View v(a, row, ctile, TL::kCols);
+        const bool starts = j == 0, ends = stop == cost;
+        float *piece = sh.pieces + ((int64_t)share * 2 + (starts ? 1 : 0)) * TL::kPiece;
+        // tiles that this column tile sees of them
+        const int j0 = max(rt.lo + max(0, j - kUnitCost), v.lo >> 4);
+        const int j1 = min(rt.lo + max(0, stop - kUnitCost), (v.hi + 15) >> 4);
+        unit_tiles<T, D, FMT, NT>(a, v, row, head, j0, j1, smem, [&](int col, int d, float4 o, float mm, float ll) {
+            if (starts && ends) {
+                finish<T, D>(a, v, head, col, d, o, mm, ll);
+            } else {
+                *reinterpret_cast<float4 *>(piece + col * D + d) = o;
+                if (d == 0) {
+                    piece[TL::kCols * D + col] = mm;
+                    piece[TL::kCols * (D + 1) + col] = ll;
+                }
+            }
+        });
+        if (starts && !ends) {
+            cut = true;
+            if (tid == 0) sh.cuts[share] = Cut{row, head, ctile, (int)((pos - j + cost - 1) / per)};
+        }
+        pos += stop - j;
+    }
+    if (!cut && tid == 0) sh.cuts[share] = Cut{-1, 0, 0, 0};
+    pdl_launch_dependents();
+}
+
+// Joins the pieces of the unit that goes on from share blockIdx.x, in order.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(256)
+attend_join_kernel(const AttendArgs a, const Shares sh)
+{
+    using TL = Tile<D, NT>;
+    pdl_wait();
+    const int share = blockIdx.x;
+    const Cut cut = sh.cuts[share];
+    if (cut.row < 0) return;
+    const View v(a, cut.row, cut.ctile, TL::kCols);
+    const int i = blockIdx.y * 256 + threadIdx.x, col = i / (D / 4), d = (i % (D / 4)) * 4;
+    if (col >= TL::kCols || v.c0 + col >= v.cols) return;
+    // piece 0 is what goes on, the others began earlier
+    auto piece = [&](int k) { return sh.pieces + ((int64_t)(share + k) * 2 + (k ? 0 : 1)) * TL::kPiece; };
+    const int n = cut.last - share + 1;
+    float mm = -INFINITY;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) mm = fmaxf(mm, piece(k)[TL::kCols * D + col]);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float ll = 0.0f;
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+        const float *p = piece(k);
+        const float mk = p[TL::kCols * D + col], f = mk == -INFINITY ? 0.0f : ex2(mk - mm);
+        const float4 x = *reinterpret_cast<const float4 *>(p + col * D + d);
+        o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
+        ll = fmaf(p[TL::kCols * (D + 1) + col], f, ll);
+    }
+    finish<T, D>(a, v, cut.head, col, d, o, mm, ll);
 }
 
 // Makes a kernel ready on the current device, once per device.
@@ -417,44 +617,94 @@ bool configure(K kern, size_t smem, bool (&done)[64])
     return true;
 }
 
+// Shares of a call, or 0 where it takes clusters: with what the planned lengths
+// can come to, each share keeps kMinShare tiles for each resident CTA.
+template <int D, int NT>
+int shares_of(const AttendArgs &a)
+{
+    using TL = Tile<D, NT>;
+    if (a.L.rows > kMaxPlanRows) return 0;
+    const int64_t ctiles = ((int64_t)a.max_new * a.group + TL::kCols - 1) / TL::kCols;
+    const int64_t span = a.window > 0 ? std::min<int64_t>(a.max_len, (int64_t)a.window + a.max_new) : a.max_len;
+    const int64_t most = ctiles * a.L.heads * a.L.rows * ((span + 15) / 16);
+    const int slots = sm_count() * TL::kResident;
+    return most >= (int64_t)slots * kMinShare ? slots : 0;
+}
+
+template <int D, int NT>
+int64_t shares_bytes(int shares)
+{
+    return (int64_t)shares * (2 * Tile<D, NT>::kPiece * (int64_t)sizeof(float) + (int64_t)sizeof(Cut));
+}
+
 template <typename T, int D, int FMT, int NT>
 int launch_t(const AttendArgs &a, cudaStream_t s)
 {
-    auto kern = attend_decode_kernel<T, D, FMT, NT>;
     using TL = Tile<D, NT>;
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(TL::kThreads);
+    cfg.dynamicSmemBytes = TL::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    cfg.attrs = attr;
+    const int shares = a.work ? shares_of<D, NT>(a) : 0;
+    if (shares > 0) {
+        auto kern = attend_shares_kernel<T, D, FMT, NT>;
+        static bool done[64] = {};
+        if (!configure(kern, TL::kSmem, done)) return BQD_ERR_CUDA;
+        Shares sh;
+        sh.pieces = static_cast<float *>(a.work);
+        sh.cuts = reinterpret_cast<Cut *>(sh.pieces + (int64_t)shares * 2 * TL::kPiece);
+        sh.count = shares;
+        cfg.gridDim = dim3((unsigned)shares);
+        if (cudaLaunchKernelEx(&cfg, kern, a, sh) != cudaSuccess) return BQD_ERR_CUDA;
+        cfg.gridDim = dim3((unsigned)shares, (TL::kCols * D / 4 + 255) / 256);
+        cfg.blockDim = dim3(256);
+        cfg.dynamicSmemBytes = 0;
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.numAttrs = 1;
+        return cuda_status(cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, NT>, a, sh));
+    }
+    auto kern = attend_cluster_kernel<T, D, FMT, NT>;
     static bool done[64] = {};
     if (!configure(kern, TL::kSmem, done)) return BQD_ERR_CUDA;
     const int64_t ctiles = ((int64_t)a.max_new * a.group + TL::kCols - 1) / TL::kCols;
     const int64_t units = ctiles * a.L.heads * a.L.rows;
     // split the keys until there are two CTAs an SM, as long as each warp
-    // keeps two tiles
+    // keeps a tile
     int S = 1;
-    while (S < kMaxSplit && units * S < 2 * sm_count() && a.max_len >= 2 * kBlock * kWarpsD * 2 * S) S *= 2;
-    cudaLaunchConfig_t cfg = {};
+    while (S < kMaxSplit && units * S < 2 * sm_count() && a.max_len >= kBlock * TL::kWarps * 2 * S) S *= 2;
     if (ctiles * S > 0x7FFFFFFF) return BQD_ERR_INVALID_ARG;
     cfg.gridDim = dim3((unsigned)(ctiles * S), (unsigned)a.L.heads, (unsigned)a.L.rows);
-    cfg.blockDim = dim3(kWarpsD * 32);
-    cfg.dynamicSmemBytes = TL::kSmem;
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = S;
     attr[0].val.clusterDim.y = 1;
     attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cuda_status(cudaLaunchKernelEx(&cfg, kern, a, S));
 }
 
+// Column tiles of 16 where there are more than 8 columns (D = 256 has no registers for them)
+bool wide(const AttendArgs &a) { return (int64_t)a.max_new * a.group > 8; }
+
 template <typename T, int FMT>
 int launch_d(const AttendArgs &a, cudaStream_t s)
 {
-    if (a.head_dim == 64) return launch_t<T, 64, FMT, 1>(a, s);
-    if (a.head_dim == 128) return launch_t<T, 128, FMT, 1>(a, s);
-    return launch_t<T, 256, FMT, 1>(a, s);
+    if (a.head_dim == 256) return launch_t<T, 256, FMT, 1>(a, s);
+    if (a.head_dim == 64) return wide(a) ? launch_t<T, 64, FMT, 2>(a, s) : launch_t<T, 64, FMT, 1>(a, s);
+    return wide(a) ? launch_t<T, 128, FMT, 2>(a, s) : launch_t<T, 128, FMT, 1>(a, s);
 }
 
 }  // namespace
+
+int64_t decode_workspace(const AttendArgs &a)
+{
+    if (a.head_dim == 256) return shares_bytes<256, 1>(shares_of<256, 1>(a));
+    if (a.head_dim == 64)
+        return wide(a) ? shares_bytes<64, 2>(shares_of<64, 2>(a)) : shares_bytes<64, 1>(shares_of<64, 1>(a));
+    return wide(a) ? shares_bytes<128, 2>(shares_of<128, 2>(a)) : shares_bytes<128, 1>(shares_of<128, 1>(a));
+}
 
 int launch_attend_decode(const AttendArgs &a, cudaStream_t s)
 {

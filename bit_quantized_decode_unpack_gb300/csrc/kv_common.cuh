@@ -148,7 +148,7 @@ struct AttendArgs {
     int dtype, format, head_dim, q_heads, group;
     int tokens, max_new, max_len, window;
     bool q_vec;               // 16-byte loads of q are possible
-    void *work;               // scratch of the staged prefill form, or nullptr
+    void *work;               // scratch of decode_workspace / prefill_workspace bytes, or nullptr
 };
 
 // Request of bqd_kv_append after host validation.
@@ -164,7 +164,8 @@ struct AppendArgs {
 int launch_append(const AppendArgs &a, cudaStream_t s);
 int launch_attend_decode(const AttendArgs &a, cudaStream_t s);
 int launch_attend_prefill(const AttendArgs &a, cudaStream_t s);
-int64_t prefill_workspace(const AttendArgs &a);  // bytes of its scratch
+int64_t decode_workspace(const AttendArgs &a);   // bytes of their scratch
+int64_t prefill_workspace(const AttendArgs &a);
 int launch_reserve(const bqd_kv_cache &c, const int32_t *counts, int32_t *base, int32_t *copies, int32_t *status,
                    cudaStream_t s);
 int launch_fork(const bqd_kv_cache &from, const bqd_kv_cache &to, const int32_t *parents, const int32_t *keep,

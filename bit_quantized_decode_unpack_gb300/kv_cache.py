@@ -266,7 +266,7 @@ class KVCache:
         else:
             _dense(lse, "lse", torch.float32, (tokens, heads), self.device)
         # scratch, from the allocator's pool of this stream: used by this call alone
-        need = self.attend_workspace(heads, max_new, max_len) if max_new * heads >= 64 else 0
+        need = self.attend_workspace(heads, max_new, max_len)
         work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         qs = q.stride()
         _check("bqd_kv_attend", self._lib.bqd_kv_attend(
