@@ -22,6 +22,9 @@ constexpr int kWarpsP = kThreadsP / 32;
 constexpr int kScan = 4;           // pages a thread looks at between barriers
 constexpr int kCopyThreads = 256;
 constexpr int kUnit = 16384;       // bytes that a CTA copies at a time
+// entries and pages up to which one CTA forks by itself: one launch instead of
+// a copy and a launch
+constexpr int64_t kSmallFork = 16384;
 
 // Exclusive prefix of v over the CTA's threads; `sum` gets the total.
 __device__ int block_prefix(int v, int *warp_sums, int &sum)
@@ -88,6 +91,7 @@ struct ReserveParams {
 __global__ void __launch_bounds__(kThreadsP)
 reserve_kernel(const ReserveParams p)
 {
+    qmvdev::pdl_launch_dependents();  // the copies' CTAs take their places and wait
     extern __shared__ int32_t dyn[];
     int32_t *last = dyn;               // [rows]: partly filled last page, or -1
     int32_t *before = dyn + p.rows;    // [rows]: pages given to the rows before
@@ -233,6 +237,7 @@ __device__ void copy_unit(const Pools &p, int src, int dst, int64_t unit)
 __global__ void __launch_bounds__(kCopyThreads)
 copy_pages_kernel(const Pools p, const int32_t *src, const int32_t *dst, int stride, int64_t n)
 {
+    qmvdev::pdl_wait();
     const int64_t per = units_of(p);
     for (int64_t u = blockIdx.x; u < n * per; u += gridDim.x) {
         const int64_t i = u / per;
@@ -249,36 +254,50 @@ struct ForkParams {
     int rows, new_rows, row_pages, page_shift, pages;
 };
 
+// What entry e of the old rows' tables, then of the new rows', does to the counts
+__device__ __forceinline__ void fork_entry(const ForkParams &p, int64_t e)
+{
+    const int64_t old_n = (int64_t)p.rows * p.row_pages;
+    const int pt = 1 << p.page_shift, cap = p.row_pages << p.page_shift;
+    if (e < old_n) {
+        const int r = (int)(e / p.row_pages), j = (int)(e % p.row_pages);
+        const int len = max(0, min(p.lens[r], cap));
+        if (j >= (len + pt - 1) >> p.page_shift) return;
+        const int page = p.table[e];
+        if ((unsigned)page < (unsigned)p.pages) atomicSub(&p.refs[page], 1);
+    } else {
+        const int64_t f = e - old_n;
+        const int i = (int)(f / p.row_pages), j = (int)(f % p.row_pages);
+        const int par = p.parents[i];
+        int len = 0;
+        if ((unsigned)par < (unsigned)p.rows) {
+            len = max(0, min(p.lens[par], cap));
+            if (p.keep) len = max(0, min(len, p.keep[i]));
+        }
+        int page = -1;
+        if (j < (len + pt - 1) >> p.page_shift) page = p.table[(int64_t)par * p.row_pages + j];
+        p.new_table[f] = page;
+        if (j == 0) p.new_lens[i] = len;
+        if ((unsigned)page < (unsigned)p.pages) atomicAdd(&p.refs[page], 1);
+    }
+}
+
 // refs already holds the old counts: take away what the old rows name, add
 // what the new rows name
 __global__ void fork_kernel(const ForkParams p)
 {
-    const int64_t old_n = (int64_t)p.rows * p.row_pages, new_n = (int64_t)p.new_rows * p.row_pages;
-    const int pt = 1 << p.page_shift, cap = p.row_pages << p.page_shift;
-    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < old_n + new_n;
-         e += (int64_t)gridDim.x * blockDim.x) {
-        if (e < old_n) {
-            const int r = (int)(e / p.row_pages), j = (int)(e % p.row_pages);
-            const int len = max(0, min(p.lens[r], cap));
-            if (j >= (len + pt - 1) >> p.page_shift) continue;
-            const int page = p.table[e];
-            if ((unsigned)page < (unsigned)p.pages) atomicSub(&p.refs[page], 1);
-        } else {
-            const int64_t f = e - old_n;
-            const int i = (int)(f / p.row_pages), j = (int)(f % p.row_pages);
-            const int par = p.parents[i];
-            int len = 0;
-            if ((unsigned)par < (unsigned)p.rows) {
-                len = max(0, min(p.lens[par], cap));
-                if (p.keep) len = max(0, min(len, p.keep[i]));
-            }
-            int page = -1;
-            if (j < (len + pt - 1) >> p.page_shift) page = p.table[(int64_t)par * p.row_pages + j];
-            p.new_table[f] = page;
-            if (j == 0) p.new_lens[i] = len;
-            if ((unsigned)page < (unsigned)p.pages) atomicAdd(&p.refs[page], 1);
-        }
-    }
+    const int64_t n = ((int64_t)p.rows + p.new_rows) * p.row_pages;
+    for (int64_t e = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; e < n; e += (int64_t)gridDim.x * blockDim.x)
+        fork_entry(p, e);
+}
+
+// The same with the copy of the old counts, in one CTA
+__global__ void __launch_bounds__(kThreadsP) fork_small_kernel(const ForkParams p, const int32_t *old_refs)
+{
+    for (int i = threadIdx.x; i < p.pages; i += kThreadsP) p.refs[i] = old_refs[i];
+    __syncthreads();
+    const int n = (p.rows + p.new_rows) * p.row_pages;
+    for (int e = threadIdx.x; e < n; e += kThreadsP) fork_entry(p, e);
 }
 
 struct CompactParams {
@@ -360,13 +379,24 @@ int shift_of(int page_tokens)
     return s;
 }
 
-int launch_copy(const Pools &p, const int32_t *src, const int32_t *dst, int stride, int64_t n, cudaStream_t s)
+// early: the kernel before it is the one that writes src and dst, and lets this
+// one be launched while it runs
+int launch_copy(const Pools &p, const int32_t *src, const int32_t *dst, int stride, int64_t n, cudaStream_t s,
+                bool early = false)
 {
     const int64_t units = n * units_of(p);
     if (units == 0) return BQD_OK;
     const unsigned grid = (unsigned)std::min<int64_t>(units, (int64_t)sm_count() * 64);
-    copy_pages_kernel<<<grid, kCopyThreads, 0, s>>>(p, src, dst, stride, n);
-    return cuda_status(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = early ? 1 : 0;
+    return cuda_status(cudaLaunchKernelEx(&cfg, copy_pages_kernel, p, src, dst, stride, n));
 }
 
 }  // namespace
@@ -378,18 +408,22 @@ int launch_reserve(const bqd_kv_cache &c, const int32_t *counts, int32_t *base, 
                     (int)c.pages, c.rows, c.row_pages, shift_of(c.page_tokens)};
     reserve_kernel<<<1, kThreadsP, 2 * sizeof(int32_t) * (size_t)c.rows, s>>>(p);
     const int st = cuda_status(cudaGetLastError());
-    return st != BQD_OK ? st : launch_copy(pools_of(c), copies, copies + 1, 2, c.rows, s);
+    return st != BQD_OK ? st : launch_copy(pools_of(c), copies, copies + 1, 2, c.rows, s, true);
 }
 
 int launch_fork(const bqd_kv_cache &from, const bqd_kv_cache &to, const int32_t *parents, const int32_t *keep,
                 cudaStream_t s)
 {
-    if (cudaMemcpyAsync(to.refs, from.refs, sizeof(int32_t) * (size_t)from.pages, cudaMemcpyDeviceToDevice, s) !=
-        cudaSuccess)
-        return BQD_ERR_CUDA;
     ForkParams p{from.table, from.lens, to.table, to.lens, to.refs, parents, keep,
                  from.rows, to.rows, from.row_pages, shift_of(from.page_tokens), (int)from.pages};
     const int64_t entries = ((int64_t)from.rows + to.rows) * from.row_pages;
+    if (entries + from.pages <= kSmallFork) {
+        fork_small_kernel<<<1, kThreadsP, 0, s>>>(p, from.refs);
+        return cuda_status(cudaGetLastError());
+    }
+    if (cudaMemcpyAsync(to.refs, from.refs, sizeof(int32_t) * (size_t)from.pages, cudaMemcpyDeviceToDevice, s) !=
+        cudaSuccess)
+        return BQD_ERR_CUDA;
     if (entries == 0) return BQD_OK;
     const unsigned grid = (unsigned)std::min<int64_t>((entries + 255) / 256, (int64_t)sm_count() * 32);
     fork_kernel<<<grid, 256, 0, s>>>(p);

@@ -31,6 +31,8 @@ from . import DTYPE_BF16, DTYPE_F16, _check, load
 
 BLOCK = 16
 FORMATS = {"int8": 1, "e4m3": 2}
+torch = None     # bound when the first cache is made: importing the package needs no torch
+_KINDS = {}      # element types of q, k and v
 PAGE_TOKENS = (16, 32, 64, 128, 256)
 HEAD_DIMS = (64, 128, 256)
 
@@ -61,9 +63,19 @@ def declare(lib):
     lib.bqd_kv_attend_workspace.restype = i64
 
 
+def _bind():
+    """The module's torch."""
+    global torch
+    if torch is None:
+        import torch as t
+        _KINDS.update({t.float16: DTYPE_F16, t.bfloat16: DTYPE_BF16})
+        torch = t
+    return torch
+
+
 def _dense(t, name, dtype, shape, device):
     """A dense tensor of this type and shape on this device (an integer array that a kernel indexes)."""
-    if t is None or t.dtype != dtype or t.device != device or tuple(t.shape) != shape or not t.is_contiguous():
+    if t is None or t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.device != device:
         got = None if t is None else f"{t.dtype} {tuple(t.shape)} on {t.device}"
         raise ValueError(f"{name}: must be a contiguous {dtype} tensor of shape {shape} on {device}, got {got}")
     return t
@@ -76,7 +88,6 @@ class _On:
         self.device, self.stream = device, stream
 
     def __enter__(self):
-        import torch
         self.a = torch.cuda.device(self.device)
         self.a.__enter__()
         self.b = torch.cuda.stream(self.stream)
@@ -95,7 +106,7 @@ class KVCache:
     table: int32 [rows, row_pages]; lens: int32 [rows]; refs: int32 [pages]."""
 
     def __init__(self, k, v, k_scales, v_scales, table, lens, refs):
-        import torch
+        _bind()
         if getattr(k, "dim", lambda: 0)() != 5 or not k.is_cuda:
             raise ValueError("k must be a CUDA tensor [layers, pages, kv_heads, page_tokens, head_dim]")
         kinds = {torch.int8: "int8", torch.uint8: "int8", torch.float8_e4m3fn: "e4m3"}
@@ -120,24 +131,26 @@ class KVCache:
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.format = kinds[k.dtype]
         self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim = layers, pages, heads, pt, d
-        self.device = dev
-        self._own(table, lens, refs)
+        self.device, self._index = dev, dev.index
+        self._lib = load()
+        self._attend, self._append = self._lib.bqd_kv_attend, self._lib.bqd_kv_append
+        self._scratch = {}  # bytes of scratch by (q heads, max_new, max_len)
+        p = lambda t: t.data_ptr() or None
+        self._own(table, lens, refs, CacheStruct(p(k), p(v), p(k_scales), p(v_scales), None, None, None, pages, layers,
+                                                 heads, d, pt, 0, table.shape[1], FORMATS[self.format], 0))
 
-    def _own(self, table, lens, refs):
+    def _own(self, table, lens, refs, c):
+        """Takes the table, lens and refs, and a struct with the rest filled in."""
         self.table, self.lens, self.refs = table, lens, refs
         self.rows, self.row_pages = table.shape
-        p = lambda t: t.data_ptr() or None
-        self._c = CacheStruct(p(self.k), p(self.v), p(self.k_scales), p(self.v_scales), p(table), p(lens), p(refs),
-                              self.pages, self.layers, self.kv_heads, self.head_dim, self.page_tokens, self.rows,
-                              self.row_pages, FORMATS[self.format], 0)
-        self._ref = ctypes.byref(self._c)
-        self._lib = load()
+        c.table, c.lens, c.refs, c.rows = table.data_ptr() or None, lens.data_ptr() or None, refs.data_ptr(), self.rows
+        self._c, self._ref = c, ctypes.byref(c)
 
     @classmethod
     def empty(cls, layers: int, pages: int, kv_heads: int, head_dim: int, rows: int, row_pages: int,
               page_tokens: int = 64, format: str = "int8", device="cuda"):
         """A cache of its own memory with every page free and every row empty."""
-        import torch
+        _bind()
         if format not in FORMATS:
             raise ValueError(f"format must be one of {sorted(FORMATS)}, got {format!r}")
         kind = torch.int8 if format == "int8" else torch.float8_e4m3fn
@@ -150,40 +163,35 @@ class KVCache:
 
     def _sibling(self, rows, out):
         """A cache over the same pools with a table, lens and refs of its own."""
-        import torch
         if out is not None:
             same = isinstance(out, KVCache) and out.rows == rows and out.row_pages == self.row_pages and \
-                all(getattr(out, n) is getattr(self, n) for n in ("k", "v", "k_scales", "v_scales"))
+                out.k is self.k and out.v is self.v and out.k_scales is self.k_scales and out.v_scales is self.v_scales
             if not same or out is self:
                 raise ValueError(f"out: must be another KVCache of {rows} rows over the same pools")
             return out
         new = object.__new__(KVCache)
-        for n in ("k", "v", "k_scales", "v_scales", "format", "layers", "pages", "kv_heads", "page_tokens",
-                  "head_dim", "device"):
-            setattr(new, n, getattr(self, n))
-        i32 = torch.int32
-        new._own(torch.empty((rows, self.row_pages), dtype=i32, device=self.device),
-                 torch.empty(rows, dtype=i32, device=self.device), torch.empty(self.pages, dtype=i32, device=self.device))
+        new.__dict__.update(self.__dict__)
+        new._scratch = {}
+        i32, dev = torch.int32, self.device
+        new._own(torch.empty((rows, self.row_pages), dtype=i32, device=dev), torch.empty(rows, dtype=i32, device=dev),
+                 torch.empty(self.pages, dtype=i32, device=dev), CacheStruct.from_buffer_copy(self._c))
         return new
 
     def _on(self, stream):
         """None, or a context that a call has to run in: another current device, or an explicit stream."""
-        import torch
-        if stream is None and torch.cuda.current_device() == self.device.index:
+        if stream is None and torch.cuda.current_device() == self._index:
             return None
         return _On(self.device, stream)
 
     def _stream(self):
-        import torch
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return torch._C._cuda_getCurrentRawStream(self._index)
 
     def _half(self, t, name, heads):
         """Element type of q, k or v: fp16 or bf16 [tokens, heads, head_dim] on the device, head_dim contiguous."""
-        import torch
         if getattr(t, "dim", lambda: 0)() != 3 or t.device != self.device:
             raise ValueError(f"{name}: must be a 3-D tensor [tokens, heads, head_dim] on {self.device}")
-        kind = DTYPE_F16 if t.dtype is torch.float16 else DTYPE_BF16 if t.dtype is torch.bfloat16 else 0
-        if not kind:
+        kind = _KINDS.get(t.dtype)
+        if kind is None:
             raise ValueError(f"{name}: dtype {t.dtype}, expected float16 or bfloat16")
         n, h, d = t.shape
         if d != self.head_dim or (heads and h != heads):
@@ -194,7 +202,6 @@ class KVCache:
 
     def _ragged(self, starts, tokens, max_new):
         """Pointer of starts and the bound of a row's new tokens."""
-        import torch
         if starts is None:
             if tokens != self.rows:
                 raise ValueError(f"without starts there is one token for each of {self.rows} rows, got {tokens}")
@@ -219,7 +226,6 @@ class KVCache:
         k, v: fp16 or bf16 [tokens, kv_heads, head_dim], any strides of token and head;
         row r's tokens go to positions base[r], base[r] + 1, ... (base of ``reserve``;
         negative: skipped).  A row has at most ``max_new`` (default: all of them)."""
-        import torch
         kind = self._half(k, "k", self.kv_heads)
         if self._half(v, "v", self.kv_heads) != kind or v.shape[0] != k.shape[0]:
             raise ValueError("k and v must have the same dtype and number of tokens")
@@ -231,7 +237,7 @@ class KVCache:
             with on:
                 return self.append(k, v, base, starts, layer=layer, max_new=max_new)
         ks, vs = k.stride(), v.stride()
-        _check("bqd_kv_append", self._lib.bqd_kv_append(
+        _check("bqd_kv_append", self._append(
             self._ref, self._layer(layer), k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1], kind,
             base.data_ptr(), at, tokens, max_new, self._stream()))
 
@@ -244,7 +250,6 @@ class KVCache:
         of each query; ``scale`` defaults to 1 / sqrt(head_dim); ``max_len`` bounds the rows'
         lengths where the caller knows them (only speed depends on it).  Returns
         (out [tokens, q_heads, head_dim], lse fp32 [tokens, q_heads])."""
-        import torch
         kind = self._half(q, "q", None)
         tokens, heads, d = q.shape
         if heads == 0 or heads % self.kv_heads:
@@ -266,10 +271,12 @@ class KVCache:
         else:
             _dense(lse, "lse", torch.float32, (tokens, heads), self.device)
         # scratch, from the allocator's pool of this stream: used by this call alone
-        need = self.attend_workspace(heads, max_new, max_len)
+        need = self._scratch.get((heads, max_new, max_len))
+        if need is None:
+            need = self._scratch[heads, max_new, max_len] = self.attend_workspace(heads, max_new, max_len)
         work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         qs = q.stride()
-        _check("bqd_kv_attend", self._lib.bqd_kv_attend(
+        _check("bqd_kv_attend", self._attend(
             self._ref, self._layer(layer), q.data_ptr(), qs[0], qs[1], kind, heads, at, tokens, max_new, max_len,
             1.0 / math.sqrt(d) if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
             work.data_ptr() if need else None, need, self._stream()))
@@ -287,19 +294,18 @@ class KVCache:
 
         Returns (base int32 [rows]: where the new tokens go, -1 where the call failed;
         status int32 [2]: missing pages and rows that outgrow the table, (0, 0) on success)."""
-        import torch
         if counts is not None:
             _dense(counts, "counts", torch.int32, (self.rows,), self.device)
         on = self._on(stream)
         if on is not None:
             with on:
                 return self.reserve(counts)
-        n = self.rows
-        buf = torch.empty(3 * n + 2, dtype=torch.int32, device=self.device)
-        base, status = buf[:n], buf[3 * n:]
-        p = buf.data_ptr()
+        base = torch.empty(self.rows, dtype=torch.int32, device=self.device)
+        status = torch.empty(2, dtype=torch.int32, device=self.device)
+        copies = torch.empty((self.rows, 2), dtype=torch.int32, device=self.device)
         _check("bqd_kv_reserve", self._lib.bqd_kv_reserve(
-            self._ref, None if counts is None else counts.data_ptr(), p, p + 4 * n, p + 12 * n, self._stream()))
+            self._ref, None if counts is None else counts.data_ptr(), base.data_ptr() or None, copies.data_ptr() or None,
+            status.data_ptr(), self._stream()))
         return base, status
 
     def fork(self, parents, keep=None, *, out=None, stream=None):
@@ -307,7 +313,6 @@ class KVCache:
         (default: all; a parent outside [0, rows) gives an empty row), with the reference
         counts that follow (bqd_kv_fork).  It takes this cache's place: of the two, only one
         may go on.  parents, keep: int32 [new rows]."""
-        import torch
         if getattr(parents, "dim", lambda: 0)() != 1:
             raise ValueError("parents must be an int32 tensor [new rows]")
         rows = parents.shape[0]
@@ -325,7 +330,6 @@ class KVCache:
 
     def truncate(self, keep, *, out=None, stream=None):
         """Each row cut to its first keep[r] tokens; pages that no row lists any more are free."""
-        import torch
         on = self._on(stream)
         if on is not None:
             with on:
@@ -335,7 +339,6 @@ class KVCache:
     def compact(self, *, out=None, stream=None):
         """Moves the live pages to the low end of the pool (bqd_kv_compact).  Returns the cache
         that takes this one's place and an int32 [1] count of the pages that moved."""
-        import torch
         on = self._on(stream)
         if on is not None:
             with on:
@@ -350,7 +353,6 @@ class KVCache:
     def copy_pages(self, src, dst, *, stream=None):
         """Copies page src[i] to page dst[i] in every layer (bqd_kv_copy_pages); int32 [n] each,
         no page in both nor twice in dst.  table and refs are the caller's to change."""
-        import torch
         if getattr(src, "dim", lambda: 0)() != 1:
             raise ValueError("src must be an int32 tensor [n]")
         n = src.shape[0]
