@@ -55,12 +55,22 @@ constexpr int kMaxPlanRows = 1024; // rows that a CTA adds up
 constexpr int kMinShare = 32;     // tiles of a share at least
 constexpr int kUnitCost = 24;     // what a unit costs beside its tiles (q, the first loads, the join), in tiles:
                                   // 32 mixed sequences 81 us with 0, 58 with 8, 45 with 24, 47 with 48
-constexpr float kGrow = 8.0f;  // a reference m is replaced when x passes it by this much
+constexpr float kGrow = 8.0f;   // a reference m is replaced when x passes it by this much
+// m of a column that has seen nothing: below every score, and finite, so that
+// neither x - m (x = -inf where masked) nor a difference of two m is NaN
+constexpr float kNothing = -3.0e38f;
 
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ float lg2(float x)
+{
+    float y;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
@@ -288,7 +298,7 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_,
     float m[NT][2], l[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
-        m[n][0] = m[n][1] = -INFINITY;
+        m[n][0] = m[n][1] = kNothing;
         l[n][0] = l[n][1] = 0.0f;
 #pragma unroll
         for (int k = 0; k < KS; ++k) acc[n][k][0] = acc[n][k][1] = acc[n][k][2] = acc[n][k][3] = 0.0f;
@@ -317,32 +327,35 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_,
         const float kscale = ksc, vscale = vsc;
         if (more) load_k(next);
 
-        const float lv = __log2f(vscale), rv = __frcp_rn(vscale);
+        // rv from lv: what lg2 is off by drops out of p / l
+        const float lv = lg2(fmaxf(vscale, 1e-37f)), rv = ex2(-lv);
         const bool whole = t0 + 15 <= p_min && (a.window == 0 || t0 > p_max - a.window);
-        uint32_t pb[NT][2];
+        bool grow = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const float f0 = cs[n][0] * kscale, f1 = cs[n][1] * kscale;
-            float x[4] = {fmaf(s[n][0], f0, lv), fmaf(s[n][1], f1, lv), fmaf(s[n][2], f0, lv), fmaf(s[n][3], f1, lv)};
+            s[n][0] = fmaf(s[n][0], f0, lv), s[n][1] = fmaf(s[n][1], f1, lv);
+            s[n][2] = fmaf(s[n][2], f0, lv), s[n][3] = fmaf(s[n][3], f1, lv);
             if (!whole) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int tok = t0 + g + 8 * (e >> 1), pp = pos[n][e & 1];
-                    if (tok > pp || (a.window > 0 && tok <= pp - a.window)) x[e] = -INFINITY;
+                    if (tok > pp || (a.window > 0 && tok <= pp - a.window)) s[n][e] = -INFINITY;
                 }
             }
-            const float x0 = fmaxf(x[0], x[2]), x1 = fmaxf(x[1], x[3]);
-            if (__any_sync(0xffffffffu, x0 > m[n][0] + kGrow || x1 > m[n][1] + kGrow)) {
-                float n0 = x0, n1 = x1;
+            grow |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kGrow || fmaxf(s[n][1], s[n][3]) > m[n][1] + kGrow;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float n0 = fmaxf(s[n][0], s[n][2]), n1 = fmaxf(s[n][1], s[n][3]);
 #pragma unroll
                 for (int o = 4; o < 32; o <<= 1) {
                     n0 = fmaxf(n0, __shfl_xor_sync(0xffffffffu, n0, o));
                     n1 = fmaxf(n1, __shfl_xor_sync(0xffffffffu, n1, o));
                 }
                 n0 = fmaxf(n0, m[n][0]), n1 = fmaxf(n1, m[n][1]);
-                // -inf - -inf: nothing yet, nothing to scale
-                const float r0 = n0 == -INFINITY ? 1.0f : ex2(m[n][0] - n0);
-                const float r1 = n1 == -INFINITY ? 1.0f : ex2(m[n][1] - n1);
+                const float r0 = ex2(m[n][0] - n0), r1 = ex2(m[n][1] - n1);
                 m[n][0] = n0, m[n][1] = n1;
                 l[n][0] *= r0, l[n][1] *= r1;
 #pragma unroll
@@ -351,8 +364,12 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_,
                     acc[n][k][1] *= r1, acc[n][k][3] *= r1;
                 }
             }
-            const float m0 = m[n][0] == -INFINITY ? 0.0f : m[n][0], m1 = m[n][1] == -INFINITY ? 0.0f : m[n][1];
-            const float e0 = ex2(x[0] - m0), e1 = ex2(x[1] - m1), e2 = ex2(x[2] - m0), e3 = ex2(x[3] - m1);
+        }
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const float e0 = ex2(s[n][0] - m[n][0]), e1 = ex2(s[n][1] - m[n][1]);
+            const float e2 = ex2(s[n][2] - m[n][0]), e3 = ex2(s[n][3] - m[n][1]);
             l[n][0] = fmaf(e0 + e2, rv, l[n][0]);
             l[n][1] = fmaf(e1 + e3, rv, l[n][1]);
             pb[n][0] = transpose8x8(Half2Of<__half>::pack(e0, e1));
@@ -417,15 +434,14 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_,
     constexpr int kQuads = TL::kCols * D / 4;
     for (int i = threadIdx.x; i < kQuads; i += kWarpsD * 32) {
         const int col = i / (D / 4), d = (i % (D / 4)) * 4;
-        float mm = -INFINITY;
+        float mm = kNothing;
 #pragma unroll
         for (int w = 0; w < kWarpsD; ++w) mm = fmaxf(mm, wm[w * TL::kCols + col]);
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float ll = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarpsD; ++w) {
-            const float mw = wm[w * TL::kCols + col];
-            const float r = mw == -INFINITY ? 0.0f : ex2(mw - mm);
+            const float r = ex2(wm[w * TL::kCols + col] - mm);
             const float4 v = *reinterpret_cast<const float4 *>(part + w * TL::kWarpFloats + col * TL::kPitch + d);
             o.x = fmaf(v.x, r, o.x), o.y = fmaf(v.y, r, o.y), o.z = fmaf(v.z, r, o.z), o.w = fmaf(v.w, r, o.w);
             ll = fmaf(wl[w * TL::kCols + col], r, ll);
@@ -464,13 +480,12 @@ attend_cluster_kernel(const AttendArgs a, int S)
     constexpr int kQuads = TL::kCols * D / 4;
     for (int i = threadIdx.x * S + rank; i < kQuads; i += TL::kThreads * S) {
         const int col = i / (D / 4), d = (i % (D / 4)) * 4;
-        float mm = -INFINITY;
+        float mm = kNothing;
         for (int r = 0; r < S; ++r) mm = fmaxf(mm, ld_cluster_f32(smem_addr(jm + col), r));
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         float ll = 0.0f;
         for (int r = 0; r < S; ++r) {
-            const float mr = ld_cluster_f32(smem_addr(jm + col), r);
-            const float f = mr == -INFINITY ? 0.0f : ex2(mr - mm);
+            const float f = ex2(ld_cluster_f32(smem_addr(jm + col), r) - mm);
             const float4 x = ld_cluster_f32x4(smem_addr(joined + col * TL::kPitch + d), r);
             o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
             ll = fmaf(ld_cluster_f32(smem_addr(jl + col), r), f, ll);
@@ -587,7 +602,7 @@ attend_join_kernel(const AttendArgs a, const Shares sh)
     // piece 0 is what goes on, the others began earlier
     auto piece = [&](int k) { return sh.pieces + ((int64_t)(share + k) * 2 + (k ? 0 : 1)) * TL::kPiece; };
     const int n = cut.last - share + 1;
-    float mm = -INFINITY;
+    float mm = kNothing;
 #pragma unroll 8
     for (int k = 0; k < n; ++k) mm = fmaxf(mm, piece(k)[TL::kCols * D + col]);
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -595,7 +610,7 @@ attend_join_kernel(const AttendArgs a, const Shares sh)
 #pragma unroll 8
     for (int k = 0; k < n; ++k) {
         const float *p = piece(k);
-        const float mk = p[TL::kCols * D + col], f = mk == -INFINITY ? 0.0f : ex2(mk - mm);
+        const float f = ex2(p[TL::kCols * D + col] - mm);
         const float4 x = *reinterpret_cast<const float4 *>(p + col * D + d);
         o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
         ll = fmaf(p[TL::kCols * (D + 1) + col], f, ll);
