@@ -131,19 +131,25 @@ extern "C" int bqd_kv_append(const bqd_kv_cache *cache, int layer, const void *k
     return launch_append(a, to_stream(stream));
 }
 
-extern "C" int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_heads, int64_t max_new, int64_t max_len)
+extern "C" int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_heads, int64_t tokens, int64_t max_new,
+                                           int64_t max_len, int64_t window)
 {
     if (check_cache(cache) != BQD_OK) return 0;
     const bqd_kv_cache &c = *cache;
-    if (q_heads < c.kv_heads || q_heads % c.kv_heads != 0 || max_new < 1 || max_len < 0) return 0;
-    if (max_new * (q_heads / c.kv_heads) >= (int64_t)1 << 30 || c.rows == 0) return 0;
+    const int64_t most = (int64_t)1 << 30;
+    if (q_heads < c.kv_heads || q_heads % c.kv_heads != 0 || max_len < 0 || window < 0 || c.rows == 0) return 0;
+    if (tokens < 1 || tokens > most || max_new < 1 || max_new > most) return 0;
+    if (max_new > tokens) max_new = tokens;
+    if (max_new * (q_heads / c.kv_heads) >= most) return 0;
     AttendArgs a;
     a.L = layer_of(c, 0);
     a.head_dim = c.head_dim;
+    a.q_heads = q_heads;
     a.group = q_heads / c.kv_heads;
+    a.tokens = (int)tokens;
     a.max_new = (int)max_new;
     a.max_len = planned_length(c, max_len);
-    a.window = 0;
+    a.window = (int)(window < most ? window : 0);
     return scratch_need(a);
 }
 

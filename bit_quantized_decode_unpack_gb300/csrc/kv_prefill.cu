@@ -147,9 +147,17 @@ struct Staged {
     int steps;      // of a row at most; 0: nothing is staged
 };
 
+// Where few query tiles face many keys, `count` CTAs share a tile's steps and
+// leave O (not divided by l) with m and l; a second kernel joins them in order.
+struct Split {
+    float *o;       // [count][tokens * q_heads][D]
+    float2 *ml;     // [count][tokens * q_heads]
+    int count;      // 1: the CTA finishes its rows itself
+};
+
 template <typename T, int D, int FMT, bool STAGED>
 __global__ void __launch_bounds__(STAGED ? kThreadsStaged : kThreadsF, 1)
-attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant__ CUtensorMap map,
+attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const __grid_constant__ CUtensorMap map,
                       unsigned long long wait_ns)
 {
     using P = Plan<D>;
@@ -170,7 +178,8 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant
     const int head = blockIdx.x, row = blockIdx.y;
     const Span span(a.starts, row, a.tokens, a.max_new);
     const int rows = span.n * a.group;
-    const int r0 = (int)(gridDim.z - 1 - blockIdx.z) * P::kRows;
+    const int share = blockIdx.z % sp.count;  // of the tile's steps
+    const int r0 = (int)((gridDim.z - 1 - blockIdx.z) / sp.count) * P::kRows;
     if (r0 >= rows) return;
     const int L = a.L.length(row);
     const RowSteps all_steps(L, span.n, a.window, KT);
@@ -181,8 +190,9 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant
     const int p_first = L - span.n;  // position of query 0
     const int hi = max(0, p_first + i_max + 1);
     const int lo = a.window > 0 ? max(0, p_first + i_min + 1 - a.window) : 0;
-    const int k_lo = lo / KT * KT;
-    const int steps = hi > k_lo ? (hi - k_lo + KT - 1) / KT : 0;
+    const int k_first = lo / KT * KT, all = hi > k_first ? (hi - k_first + KT - 1) / KT : 0;
+    const int from = (int)((int64_t)all * share / sp.count), steps = (int)((int64_t)all * (share + 1) / sp.count) - from;
+    const int k_lo = k_first + from * KT;
 
     auto bar = [&](int i) { return smem_addr(&bars[i]); };
     auto k_full = [&](int j) { return bar(j % kStages); };
@@ -233,58 +243,68 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant
         const int trow = (warp & 3) * 32 + lane;
         const int r = r0 + w * 128 + trow;
         if (w < tiles) {
-            // ---- q: scaled by 2^-e into fp16 (e of the row's largest magnitude) ----
             const bool real = r < rows;
-            const int token = span.lo + (real ? r / a.group : 0);
-            const int hq = head * a.group + (real ? r % a.group : 0);
             const int pos = real ? p_first + r / a.group : -1;
-            const T *q = static_cast<const T *>(a.q) + (int64_t)token * a.q_token + (int64_t)hq * a.q_head;
-            const uint32_t q_at = base + w * (P::kPanels * P::kPanelQ) + trow * 128;
-            uint32_t top = 0;
-            auto load = [&](int u) {  // dims 8u .. 8u + 7
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (real) {
-                    if (a.q_vec) {
-                        v = __ldg(reinterpret_cast<const uint4 *>(q) + u);
-                    } else {
-                        const unsigned short *s = reinterpret_cast<const unsigned short *>(q) + 8 * u;
-                        uint32_t x[4];
+            const uint32_t q_tile = base + w * (P::kPanels * P::kPanelQ);
+            const int row0 = (warp & 3) * 32;  // the warp's rows of the tile
+            // ---- q: scaled by 2^-e into fp16 (e of the row's largest magnitude) ----
+            // D / 8 lanes take a row, 16 bytes each, eight passes in flight (one row a thread took
+            // 8 us: each load touched 32 rows)
+            constexpr int kRowLanes = D / 8, kRowsPass = 32 / kRowLanes, kPasses = kRowLanes;
+            float cs = 1.0f;  // of this thread's row: |f| 2^e
+#pragma unroll 1
+            for (int i0 = 0; i0 < kPasses; i0 += 8) {
+                uint4 v[8];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            x[i] = (uint32_t)__ldg(s + 2 * i) | ((uint32_t)__ldg(s + 2 * i + 1) << 16);
-                        v = make_uint4(x[0], x[1], x[2], x[3]);
+                for (int i = 0; i < 8; ++i) {
+                    const int rr = r0 + w * 128 + row0 + (i0 + i) * kRowsPass + lane / kRowLanes;
+                    v[i] = make_uint4(0, 0, 0, 0);
+                    if (rr < rows) {
+                        const T *q = static_cast<const T *>(a.q) + (int64_t)(span.lo + rr / a.group) * a.q_token +
+                                     (int64_t)(head * a.group + rr % a.group) * a.q_head + lane % kRowLanes * 8;
+                        if (a.q_vec) {
+                            v[i] = __ldg(reinterpret_cast<const uint4 *>(q));
+                        } else {
+                            const unsigned short *u = reinterpret_cast<const unsigned short *>(q);
+                            uint32_t x[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                x[k] = (uint32_t)__ldg(u + 2 * k) | ((uint32_t)__ldg(u + 2 * k + 1) << 16);
+                            v[i] = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
                     }
                 }
-                return v;
-            };
-            uint32_t mx = 0;
-#pragma unroll 8
-            for (int u = 0; u < D / 8; ++u) {
-                const uint4 v = load(u);
-                mx = __vmaxu2(__vmaxu2(mx, v.x & 0x7FFF7FFFu), v.y & 0x7FFF7FFFu);
-                mx = __vmaxu2(__vmaxu2(mx, v.z & 0x7FFF7FFFu), v.w & 0x7FFF7FFFu);
-            }
-            top = max(mx & 0xFFFFu, mx >> 16);
-            int e = 0;
-            if (top != 0 && top < H::kInf)
-                e = max(-100, min(126, (int)((__float_as_uint(H::f1(top)) >> 23) & 0xFF) - 127));
-            // the sign of the scale goes with q, so that a larger product is a larger score
-            const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);
-            const float cs = fabsf(a.scale) * __uint_as_float((uint32_t)(127 + e) << 23);
-#pragma unroll 8
-            for (int u = 0; u < D / 8; ++u) {
-                const uint4 v = load(u);
-                uint32_t h[4];
-                const uint32_t x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 f = H::f2(x[i]);
-                    h[i] = Half2Of<__half>::pack(f.x * down, f.y * down);
+                for (int i = 0; i < 8; ++i) {
+                    const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t mx = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu),
+                                           __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
+                    uint32_t top = max(mx & 0xFFFFu, mx >> 16);
+#pragma unroll
+                    for (int o = 1; o < kRowLanes; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    int e = 0;
+                    if (top != 0 && top < H::kInf)
+                        e = max(-100, min(126, (int)((__float_as_uint(H::f1(top)) >> 23) & 0xFF) - 127));
+                    // the sign of the scale goes with q, so that a larger product is a larger score
+                    const float down = copysignf(__uint_as_float((uint32_t)(127 - e) << 23), a.scale);
+                    const float up = fabsf(a.scale) * __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+                    for (int h = 0; h < kRowsPass; ++h) {
+                        const float of_row = __shfl_sync(0xffffffffu, up, h * kRowLanes);
+                        if (lane == (i0 + i) * kRowsPass + h) cs = of_row;
+                    }
+                    uint32_t h4[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = H::f2(x[k]);
+                        h4[k] = Half2Of<__half>::pack(f.x * down, f.y * down);
+                    }
+                    const int tr = row0 + (i0 + i) * kRowsPass + lane / kRowLanes, u = lane % kRowLanes;
+                    const uint32_t at = q_tile + (u >> 3) * P::kPanelQ + tr * 128 + (((u & 7) ^ (tr & 7)) << 4);
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(h4[0]), "r"(h4[1]), "r"(h4[2]),
+                                 "r"(h4[3])
+                                 : "memory");
                 }
-                const uint32_t at = q_at + (u >> 3) * P::kPanelQ + (((u & 7) ^ (trow & 7)) << 4);
-                asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(h[0]), "r"(h[1]), "r"(h[2]),
-                             "r"(h[3])
-                             : "memory");
             }
             mbar_arrive(q_full);
 
@@ -401,8 +421,12 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant
             if (ok && steps > 0) ok = __all_sync(0xffffffffu, wait(o_full(w), 0));
             if (ok) {
                 fence_after();
+                // O goes through this warp's part of the tile's Q (every MMA that reads it is done),
+                // 32 columns at a time, so that rows are written in whole sectors
+                const bool split = sp.count > 1;
+                if (split) pdl_launch_dependents();
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                T *out = static_cast<T *>(a.out) + ((int64_t)token * a.q_heads + hq) * D;
+                const uint32_t buf = q_tile + (warp & 3) * 4096;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -413,20 +437,59 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant
 #pragma unroll
                         for (int i = 0; i < 32; ++i) o[i] = 0;
                     }
-                    if (real) {
+                    if (!split) {
 #pragma unroll
-                        for (int i = 0; i < 32; i += 8) {
-                            uint32_t h[4];
+                        for (int i = 0; i < 32; ++i) o[i] = l == 0.0f ? 0u : __float_as_uint(__uint_as_float(o[i]) * inv);
+                    }
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                h[k] = H::pack(l == 0.0f ? 0.0f : __uint_as_float(o[i + 2 * k]) * inv,
-                                               l == 0.0f ? 0.0f : __uint_as_float(o[i + 2 * k + 1]) * inv);
-                            *reinterpret_cast<uint4 *>(out + 32 * c + i) = make_uint4(h[0], h[1], h[2], h[3]);
+                    for (int u = 0; u < 8; ++u)
+                        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(buf + lane * 128 + ((u ^ (lane & 7)) << 4)),
+                                     "r"(o[4 * u]), "r"(o[4 * u + 1]), "r"(o[4 * u + 2]), "r"(o[4 * u + 3])
+                                     : "memory");
+                    __syncwarp();
+                    auto get = [&](int tr, int u) {
+                        uint4 x;
+                        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                                     : "r"(buf + tr * 128 + ((u ^ (tr & 7)) << 4))
+                                     : "memory");
+                        return x;
+                    };
+                    auto row_of = [&](int tr) {  // of the output; -1: none
+                        const int rr = r0 + w * 128 + row0 + tr;
+                        return rr < rows ? (int64_t)(span.lo + rr / a.group) * a.q_heads + head * a.group + rr % a.group : -1;
+                    };
+                    if (split) {
+#pragma unroll 2
+                        for (int i = 0; i < 8; ++i) {
+                            const int tr = i * 4 + (lane >> 3), u = lane & 7;
+                            const int64_t to = row_of(tr);
+                            const uint4 x = get(tr, u);
+                            if (to >= 0)
+                                *reinterpret_cast<uint4 *>(sp.o + ((int64_t)share * a.tokens * a.q_heads + to) * D + 32 * c +
+                                                           4 * u) = x;
+                        }
+                    } else {
+#pragma unroll 2
+                        for (int i = 0; i < 4; ++i) {
+                            const int tr = i * 8 + (lane >> 2), u = lane & 3;
+                            const int64_t to = row_of(tr);
+                            const uint4 x = get(tr, 2 * u), y = get(tr, 2 * u + 1);
+                            if (to >= 0)
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to * D + 32 * c + 8 * u) =
+                                    make_uint4(H::pack(__uint_as_float(x.x), __uint_as_float(x.y)),
+                                               H::pack(__uint_as_float(x.z), __uint_as_float(x.w)),
+                                               H::pack(__uint_as_float(y.x), __uint_as_float(y.y)),
+                                               H::pack(__uint_as_float(y.z), __uint_as_float(y.w)));
                         }
                     }
+                    __syncwarp();
                 }
-                if (real && a.lse)
-                    a.lse[(int64_t)token * a.q_heads + hq] =
+                const int64_t out_row = (int64_t)(span.lo + (real ? r / a.group : 0)) * a.q_heads + head * a.group +
+                                        (real ? r % a.group : 0);
+                if (real && split) sp.ml[(int64_t)share * a.tokens * a.q_heads + out_row] = make_float2(m, l);
+                else if (real && a.lse)
+                    a.lse[out_row] =
                         l == 0.0f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
             }
         }
@@ -637,6 +700,37 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const __grid_constant
     if (warp == kMmaWarp) tmem_dealloc(tmem, P::kCols);
 }
 
+// Joins the shares of every query and head of a row, in order
+template <typename T, int D>
+__global__ void __launch_bounds__(256)
+join_kernel(const AttendArgs a, const Split sp)
+{
+    using H = Half2Of<T>;
+    pdl_wait();
+    const Span span(a.starts, blockIdx.y, a.tokens, a.max_new);
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, at = i / (D / 4);
+    const int d = (int)(i % (D / 4)) * 4;
+    if (at >= (int64_t)span.n * a.q_heads) return;
+    const int64_t row = (int64_t)span.lo * a.q_heads + at, all = (int64_t)a.tokens * a.q_heads;
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int k = 0; k < sp.count; ++k) m = fmaxf(m, sp.ml[k * all + row].x);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.0f;
+#pragma unroll 4
+    for (int k = 0; k < sp.count; ++k) {
+        const float2 ml = sp.ml[k * all + row];
+        const float f = ml.x == -INFINITY ? (ml.y == 0.0f ? 0.0f : 1.0f) : ex2(ml.x - m);  // (l is NaN where q is)
+        const float4 x = *reinterpret_cast<const float4 *>(sp.o + (k * all + row) * D + d);
+        o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
+        l = fmaf(ml.y, f, l);
+    }
+    const float r = l == 0.0f ? 0.0f : 1.0f / l;
+    T *to = static_cast<T *>(a.out) + row * D + d;
+    *reinterpret_cast<uint2 *>(to) = make_uint2(H::pack(o.x * r, o.y * r), H::pack(o.z * r, o.w * r));
+    if (a.lse && d == 0) a.lse[row] = l == 0.0f ? -INFINITY : 0.69314718055994531f * (m + log2f(l));
+}
+
 // Codes to fp16 tiles for the staged form: one CTA a tile (K or V of one step),
 // as the MMAs will read it; the codes of a row are converted once for all of
 // its query tiles.
@@ -720,11 +814,40 @@ int staged_steps(const AttendArgs &a)
 {
     return a.max_len / Plan<D>::KT + 2;  // a window's first step may start before its keys
 }
+// CTAs that share a query tile's steps: the count with the least time, in steps
+// of a full tile, over the waves of CTAs (one an SM).  A CTA costs about three
+// steps to begin and end, and to leave and join its O three and a half more
+// (2 x 128 KB at an SM's share of the bandwidth): 64 queries at 8192 keys, 48
+// heads: 129 us with one, 31 us with nine.
+template <int D>
+int splits_of(const AttendArgs &a)
+{
+    using P = Plan<D>;
+    const int64_t rows = (int64_t)a.max_new * a.group;
+    const int64_t ctas = (rows + P::kRows - 1) / P::kRows * a.L.heads * a.L.rows;
+    const int64_t span = a.window > 0 ? std::min<int64_t>(a.max_len, (int64_t)a.window + a.max_new) : a.max_len;
+    const double steps = (double)(span + P::KT - 1) / P::KT;
+    const int sms = sm_count();
+    int best = 1;
+    double least = 1e30;
+    for (int n = 1; n <= 16 && (n == 1 || steps >= 4 * n); ++n) {
+        const double cost = (double)((ctas * n + sms - 1) / sms) * (steps / n + (n == 1 ? 3.0 : 6.5));
+        if (cost < least) least = cost, best = n;
+    }
+    return best;
+}
+
+// Bytes of the scratch: staged tiles and their scales, then the shares
 template <int D>
 int64_t staged_bytes(const AttendArgs &a)
 {
     using P = Plan<D>;
     return (int64_t)a.L.rows * a.L.heads * staged_steps<D>(a) * (2 * (int64_t)P::kKV + P::kBlocks * 8);
+}
+template <int D>
+int64_t split_bytes(const AttendArgs &a, int splits)
+{
+    return splits > 1 ? (int64_t)splits * a.tokens * a.q_heads * (D * 4 + 8) : 0;
 }
 
 template <typename T, int D, int FMT>
@@ -738,8 +861,10 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
     const int64_t rows = (int64_t)a.max_new * a.group;
     const int64_t q_tiles = (rows + P::kRows - 1) / P::kRows;
     if (q_tiles > 65535) return BQD_ERR_INVALID_ARG;
-    const dim3 grid((unsigned)a.L.heads, (unsigned)a.L.rows, (unsigned)q_tiles);
     Staged st = {nullptr, nullptr, 0};
+    Split sp = {nullptr, nullptr, a.work ? splits_of<D>(a) : 1};
+    if (q_tiles * sp.count > 65535) sp.count = 1;
+    const dim3 grid((unsigned)a.L.heads, (unsigned)a.L.rows, (unsigned)(q_tiles * sp.count));
     CUtensorMap map = {};
     if (a.work) {
         st.steps = staged_steps<D>(a);
@@ -755,13 +880,26 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return BQD_ERR_CUDA;
         stage_kernel<D, FMT><<<dim3(2 * st.steps, a.L.heads, a.L.rows), 256, 0, s>>>(a, st);
-        staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, map, opt_wait_ns());
-        // a row can only need more steps than planned where the table's capacity does
-        const int64_t capacity = (int64_t)a.L.row_pages << a.L.page_shift;
-        if ((int64_t)st.steps * P::KT >= capacity) return cuda_status(cudaGetLastError());
+        uint8_t *end = static_cast<uint8_t *>(a.work) + staged_bytes<D>(a);
+        sp.o = reinterpret_cast<float *>(end);
+        sp.ml = reinterpret_cast<float2 *>(sp.o + (int64_t)sp.count * a.tokens * a.q_heads * D);
+        staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, sp, map, opt_wait_ns());
     }
-    direct<<<grid, kThreadsF, P::kSmem, s>>>(a, st, map, opt_wait_ns());
-    return cuda_status(cudaGetLastError());
+    // a row can only need more steps than planned where the table's capacity does
+    const int64_t capacity = (int64_t)a.L.row_pages << a.L.page_shift;
+    if ((int64_t)st.steps * P::KT < capacity) direct<<<grid, kThreadsF, P::kSmem, s>>>(a, st, sp, map, opt_wait_ns());
+    if (sp.count == 1) return cuda_status(cudaGetLastError());
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(((int64_t)a.max_new * a.q_heads * (D / 4) + 255) / 256), (unsigned)a.L.rows);
+    cfg.blockDim = dim3(256);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t launched = cudaGetLastError();
+    return cuda_status(launched != cudaSuccess ? launched : cudaLaunchKernelEx(&cfg, join_kernel<T, D>, a, sp));
 }
 
 template <typename T, int FMT>
@@ -776,7 +914,13 @@ int launch_d(const AttendArgs &a, cudaStream_t s)
 
 int64_t prefill_workspace(const AttendArgs &a)
 {
-    return a.head_dim == 64 ? staged_bytes<64>(a) : a.head_dim == 128 ? staged_bytes<128>(a) : staged_bytes<256>(a);
+    auto bytes = [&](auto d) {
+        constexpr int D = decltype(d)::value;
+        return staged_bytes<D>(a) + split_bytes<D>(a, splits_of<D>(a));
+    };
+    return a.head_dim == 64    ? bytes(std::integral_constant<int, 64>())
+           : a.head_dim == 128 ? bytes(std::integral_constant<int, 128>())
+                               : bytes(std::integral_constant<int, 256>());
 }
 
 int launch_attend_prefill(const AttendArgs &a, cudaStream_t s)

@@ -53,7 +53,7 @@ def declare(lib):
     lib.bqd_kv_append.argtypes = [cp, i32, vp, i64, i64, vp, i64, i64, i32, vp, vp, i64, i64, vp]
     lib.bqd_kv_attend.argtypes = [cp, i32, vp, i64, i64, i32, i32, vp, i64, i64, i64, ctypes.c_float, i64, vp, vp, vp,
                                   i64, vp]
-    lib.bqd_kv_attend_workspace.argtypes = [cp, i32, i64, i64]
+    lib.bqd_kv_attend_workspace.argtypes = [cp, i32, i64, i64, i64, i64]
     lib.bqd_kv_reserve.argtypes = [cp, vp, vp, vp, vp, vp]
     lib.bqd_kv_fork.argtypes = [cp, cp, vp, vp, vp]
     lib.bqd_kv_compact.argtypes = [cp, cp, vp, vp, vp]
@@ -134,7 +134,7 @@ class KVCache:
         self.device, self._index = dev, dev.index
         self._lib = load()
         self._attend, self._append = self._lib.bqd_kv_attend, self._lib.bqd_kv_append
-        self._scratch = {}  # bytes of scratch by (q heads, max_new, max_len)
+        self._need = (None, 0)  # the last call's sizes and bytes of scratch
         p = lambda t: t.data_ptr() or None
         self._own(table, lens, refs, CacheStruct(p(k), p(v), p(k_scales), p(v_scales), None, None, None, pages, layers,
                                                  heads, d, pt, 0, table.shape[1], FORMATS[self.format], 0))
@@ -171,7 +171,7 @@ class KVCache:
             return out
         new = object.__new__(KVCache)
         new.__dict__.update(self.__dict__)
-        new._scratch = {}
+        new._need = (None, 0)
         i32, dev = torch.int32, self.device
         new._own(torch.empty((rows, self.row_pages), dtype=i32, device=dev), torch.empty(rows, dtype=i32, device=dev),
                  torch.empty(self.pages, dtype=i32, device=dev), CacheStruct.from_buffer_copy(self._c))
@@ -271,9 +271,11 @@ class KVCache:
         else:
             _dense(lse, "lse", torch.float32, (tokens, heads), self.device)
         # scratch, from the allocator's pool of this stream: used by this call alone
-        need = self._scratch.get((heads, max_new, max_len))
-        if need is None:
-            need = self._scratch[heads, max_new, max_len] = self.attend_workspace(heads, max_new, max_len)
+        need = self._need
+        if need[0] != (heads, tokens, max_new, max_len, window):
+            sizes = (heads, tokens, max_new, max_len, window)
+            need = self._need = (sizes, self.attend_workspace(*sizes))
+        need = need[1]
         work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         qs = q.stride()
         _check("bqd_kv_attend", self._attend(
@@ -282,9 +284,9 @@ class KVCache:
             work.data_ptr() if need else None, need, self._stream()))
         return out, lse
 
-    def attend_workspace(self, q_heads: int, max_new: int, max_len: int = 0) -> int:
+    def attend_workspace(self, q_heads: int, tokens: int, max_new: int, max_len: int = 0, window: int = 0) -> int:
         """Bytes of scratch that ``attend`` takes for such a call (bqd_kv_attend_workspace)."""
-        return self._lib.bqd_kv_attend_workspace(self._ref, q_heads, max_new, max_len)
+        return self._lib.bqd_kv_attend_workspace(self._ref, q_heads, tokens, max_new, max_len, window)
 
     # ---- pages -------------------------------------------------------------------
 

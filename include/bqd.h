@@ -299,15 +299,17 @@ int bqd_kv_append(const bqd_kv_cache *cache, int layer, const void *k, int64_t k
  *           planned for (0: the table's capacity); longer rows stay correct
  *   scale   finite;  window >= 0 (0: none)
  *   work    device scratch, 16-byte aligned, of work_bytes bytes, or NULL with
- *           0.  bqd_kv_attend_workspace (host-only) gives the bytes with which
- *           a call of many queries converts each row's codes once instead of
- *           once for each tile of queries; with less, work is not used.  The
- *           answer is correct either way, and nothing is kept in it.
+ *           0.  bqd_kv_attend_workspace (host-only) gives the bytes that a
+ *           call with the same sizes takes to share its keys evenly between
+ *           CTAs, and with many queries to convert each row's codes once
+ *           instead of once for each tile of queries; with less, work is not
+ *           used.  The answer is correct either way, and nothing is kept in it.
  * Returns BQD_OK, BQD_ERR_INVALID_ARG, BQD_ERR_ALIGNMENT or BQD_ERR_CUDA;
  * bqd_kv_attend_workspace returns 0 where no scratch is of use or the
  * arguments are invalid.
  */
-int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_heads, int64_t max_new, int64_t max_len);
+int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_heads, int64_t tokens, int64_t max_new,
+                                int64_t max_len, int64_t window);
 int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride,
                   int64_t q_head_stride, int dtype, int q_heads, const int32_t *starts, int64_t tokens,
                   int64_t max_new, int64_t max_len, float scale, int64_t window, void *out, float *lse,

@@ -83,6 +83,35 @@ def test_any_hint_of_the_length_gives_the_same_answer(max_len, news):
     _compare(c, q, qd, news, "float16", max_len=max_len)
 
 
+@pytest.mark.parametrize("d,fmt", [(64, "e4m3"), (128, "int8"), (256, "int8")])
+@pytest.mark.parametrize("window", [0, 900])
+def test_few_queries_far_behind_in_a_long_row(d, fmt, window):
+    """A chunk of queries whose tiles' keys several CTAs share, beside an empty row, a short one and
+    queries before the first key."""
+    rng = np.random.default_rng(16)
+    lens, news = [2500, 0, 9, 1700], [40, 30, 33, 64]
+    c = random_cache(rng, lens, heads=1, d=d, pt=64, fmt=fmt)
+    q, qd = rounded(rng.standard_normal((sum(news), 3, d)), "bfloat16")
+    _compare(c, q, qd, news, "bfloat16", window=window)
+    got = _run(c, q, news, window=window)
+    again = _run(c, q, news, window=window, max_len=1000)  # the first row is longer than planned
+    want, _, bound, _ = okv.attend(c, qd, starts_of(news), 0, None, window)
+    assert np.all(np.abs(again[0] - want) <= bound * 1.01 + BF16_HALF * np.abs(want) + 2.0 ** -25)
+    np.testing.assert_array_equal(got[0], _run(c, q, news, window=window)[0])
+
+
+@pytest.mark.parametrize("heads", [1, 4])
+@pytest.mark.parametrize("grp,news", [(4, [1] * 6), (6, [3, 1, 4, 0, 2, 2])])
+def test_shares_of_mixed_lengths(heads, grp, news):
+    """Rows of very different lengths, so that the equal shares cut units at every place, and rows
+    shorter than what a unit costs."""
+    rng = np.random.default_rng(17)
+    lens = [2600, 5, 0, 700, 17, 1300]
+    c = random_cache(rng, lens, heads=heads, d=64, pt=16, row_pages=4000)  # planned long: shares
+    q, qd = rounded(rng.standard_normal((sum(news), heads * grp, 64)), "float16")
+    _compare(c, q, qd, None if set(news) == {1} else news, "float16")
+
+
 @pytest.mark.parametrize("n", [1, 100])
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 def test_scales_far_apart(dtype, n):

@@ -88,13 +88,15 @@ def test_append(lib, kw, want):
 
 def test_workspace(lib):
     r = ctypes.byref(_cache())
-    w = lib.bqd_kv_attend_workspace
-    assert w(r, 4, 1, 0) == 0                                    # few queries need none
-    assert w(r, 4, 4096, 200) >= 3 * 2 * 200 * 2 * 128 * 2       # fp16 K and V of every row and head
-    assert w(r, 4, 4096, 100) < w(r, 4, 4096, 256) == w(r, 4, 4096, 0) == w(r, 4, 4096, 10 ** 9)
-    for bad in ((r, 3, 4096, 0), (r, 0, 4096, 0), (r, 4, 0, 0), (r, 4, 4096, -1), (r, 4, 1 << 40, 0),
-                (ctypes.byref(_cache(pages=0)), 4, 4096, 0), (None, 4, 4096, 0)):
+    w = lambda *x: lib.bqd_kv_attend_workspace(*x, 0)
+    assert w(r, 4, 3, 1, 0) == 0                                       # few queries and keys need none
+    assert w(r, 4, 9000, 4096, 200) >= 3 * 2 * 200 * 2 * 128 * 2       # fp16 K and V of every row and head
+    assert w(r, 4, 9000, 4096, 100) < w(r, 4, 9000, 4096, 256) == w(r, 4, 9000, 4096, 0) == w(r, 4, 9000, 4096, 10 ** 9)
+    assert w(r, 4, 4096, 10 ** 6, 0) == w(r, 4, 4096, 4096, 0)
+    for bad in ((r, 3, 9000, 4096, 0), (r, 0, 9000, 4096, 0), (r, 4, 9000, 0, 0), (r, 4, 0, 4096, 0), (r, 4, 9000, 4096, -1),
+                (r, 4, 1 << 40, 1 << 40, 0), (ctypes.byref(_cache(pages=0)), 4, 9000, 4096, 0), (None, 4, 9000, 4096, 0)):
         assert w(*bad) == 0
+    assert lib.bqd_kv_attend_workspace(r, 4, 9000, 4096, 0, -1) == 0
 
 
 def test_pages(lib):
