@@ -248,20 +248,23 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
             const uint32_t q_tile = base + w * (P::kPanels * P::kPanelQ);
             const int row0 = (warp & 3) * 32;  // the warp's rows of the tile
             // ---- q: scaled by 2^-e into fp16 (e of the row's largest magnitude) ----
-            // D / 8 lanes take a row, 16 bytes each, eight passes in flight (one row a thread took
-            // 8 us: each load touched 32 rows)
+            // D / 8 lanes take a row, 16 bytes each, up to 16 passes in flight (one row a thread
+            // took 8 us: each load touched 32 rows)
             constexpr int kRowLanes = D / 8, kRowsPass = 32 / kRowLanes, kPasses = kRowLanes;
+            constexpr int kFlight = kPasses < 16 ? kPasses : 16;
+            const unsigned group = a.group;
             float cs = 1.0f;  // of this thread's row: |f| 2^e
 #pragma unroll 1
-            for (int i0 = 0; i0 < kPasses; i0 += 8) {
-                uint4 v[8];
+            for (int i0 = 0; i0 < kPasses; i0 += kFlight) {
+                uint4 v[kFlight];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int rr = r0 + w * 128 + row0 + (i0 + i) * kRowsPass + lane / kRowLanes;
+                for (int i = 0; i < kFlight; ++i) {
+                    const unsigned rr = r0 + w * 128 + row0 + (i0 + i) * kRowsPass + lane / kRowLanes;
                     v[i] = make_uint4(0, 0, 0, 0);
-                    if (rr < rows) {
-                        const T *q = static_cast<const T *>(a.q) + (int64_t)(span.lo + rr / a.group) * a.q_token +
-                                     (int64_t)(head * a.group + rr % a.group) * a.q_head + lane % kRowLanes * 8;
+                    if (rr < (unsigned)rows) {
+                        const unsigned i_q = rr / group;
+                        const T *q = static_cast<const T *>(a.q) + (int64_t)(span.lo + i_q) * a.q_token +
+                                     (int64_t)(head * group + rr - i_q * group) * a.q_head + lane % kRowLanes * 8;
                         if (a.q_vec) {
                             v[i] = __ldg(reinterpret_cast<const uint4 *>(q));
                         } else {
@@ -275,7 +278,7 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                     }
                 }
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < kFlight; ++i) {
                     const uint32_t x[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
                     uint32_t mx = __vmaxu2(__vmaxu2(x[0] & 0x7FFF7FFFu, x[1] & 0x7FFF7FFFu),
                                            __vmaxu2(x[2] & 0x7FFF7FFFu, x[3] & 0x7FFF7FFFu));
@@ -427,6 +430,14 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                 if (split) pdl_launch_dependents();
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 const uint32_t buf = q_tile + (warp & 3) * 4096;
+                // the rows of the output that this lane writes, in fp32 or rounded; -1: none
+                int64_t to[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const unsigned rr = r0 + w * 128 + row0 + (split ? i * 4 + (lane >> 3) : (i & 3) * 8 + (lane >> 2));
+                    const unsigned i_q = rr / group;
+                    to[i] = rr < (unsigned)rows ? (int64_t)(span.lo + i_q) * a.q_heads + head * group + rr - i_q * group : -1;
+                }
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t o[32];
@@ -455,28 +466,22 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                                      : "memory");
                         return x;
                     };
-                    auto row_of = [&](int tr) {  // of the output; -1: none
-                        const int rr = r0 + w * 128 + row0 + tr;
-                        return rr < rows ? (int64_t)(span.lo + rr / a.group) * a.q_heads + head * a.group + rr % a.group : -1;
-                    };
                     if (split) {
-#pragma unroll 2
+#pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const int tr = i * 4 + (lane >> 3), u = lane & 7;
-                            const int64_t to = row_of(tr);
                             const uint4 x = get(tr, u);
-                            if (to >= 0)
-                                *reinterpret_cast<uint4 *>(sp.o + ((int64_t)share * a.tokens * a.q_heads + to) * D + 32 * c +
-                                                           4 * u) = x;
+                            if (to[i] >= 0)
+                                *reinterpret_cast<uint4 *>(sp.o + ((int64_t)share * a.tokens * a.q_heads + to[i]) * D +
+                                                           32 * c + 4 * u) = x;
                         }
                     } else {
-#pragma unroll 2
+#pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const int tr = i * 8 + (lane >> 2), u = lane & 3;
-                            const int64_t to = row_of(tr);
                             const uint4 x = get(tr, 2 * u), y = get(tr, 2 * u + 1);
-                            if (to >= 0)
-                                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to * D + 32 * c + 8 * u) =
+                            if (to[i] >= 0)
+                                *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + to[i] * D + 32 * c + 8 * u) =
                                     make_uint4(H::pack(__uint_as_float(x.x), __uint_as_float(x.y)),
                                                H::pack(__uint_as_float(x.z), __uint_as_float(x.w)),
                                                H::pack(__uint_as_float(y.x), __uint_as_float(y.y)),
