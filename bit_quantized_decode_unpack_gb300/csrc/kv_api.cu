@@ -88,8 +88,12 @@ int planned_length(const bqd_kv_cache &c, int64_t max_len)
     return (int)(max_len > 0 && max_len < capacity ? max_len : capacity);
 }
 
-// queries enough for tiles of 128 (query, head) rows on the tensor cores
-bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group >= 64; }
+// Queries enough for 128-row tiles on tcgen05.  The other kernel reads the keys
+// once for each 16 (query, head) columns (8 with head_dim 256).  Measured with 8
+// sequences of 8000 tokens, head_dim 64 / 128 / 256, it takes 54 / 86 / 135 us at
+// 48 columns and 79 / 119 / 196 at 60 to 66; the tiles 64 / 103 / 94 at any.  At
+// 30 columns of 256 it takes 95.
+bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 32 : 48); }
 
 // bytes of scratch that a call is better with, or 0
 int64_t scratch_need(const AttendArgs &a)

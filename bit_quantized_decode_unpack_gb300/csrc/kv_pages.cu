@@ -7,7 +7,10 @@
 // state alone and the pool stays dense without a free list.  The only atomics
 // are integer counts, whose order does not matter.  Planning touches 4 bytes a
 // page and a table entry and is bound by latency; moving pages is a copy bound
-// by memory (16-byte accesses, 64 bytes a thread in flight).
+// by memory (16-byte accesses, 64 bytes a thread in flight): 525 MB of moves with
+// their plan 97 us (5431 GB/s, 81% of a measured copy; about 8 us are the plan).
+// 64 beams of 16 parents with their copies: 19 us on the GPU in three launches,
+// 32 us a call of fork and reserve from Python.
 #include <algorithm>
 
 #include "kv_common.cuh"

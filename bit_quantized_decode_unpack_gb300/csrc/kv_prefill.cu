@@ -12,21 +12,35 @@
 // Rows of a tile are (query, head of the group) pairs, so a tile of 128 rows
 // reads each K and V code once for the whole group.  A CTA owns two tiles of
 // 128 rows (one for head_dim 256, and where there are no more rows) and walks
-// the keys in steps of KT.  Roles:
+// the keys in steps of KT.  Two forms share everything but what fills the K and
+// V tiles:
+//   staged   a first kernel converts a row's codes to fp16 tiles in scratch, once
+//            for all of its query tiles, and one thread copies them by TMA.  For
+//            calls of several query tiles.
+//   direct   seven warps convert the codes in the kernel: for one query tile a
+//            row, calls without scratch, and rows longer than planned.  Their
+//            code and the softmax's share the instruction cache and the issue
+//            slots: 2048 queries at 8192 keys take 311 us staged, 545 direct.
+// K and V tiles have the same layout ([64-dim panel][key] rows of 128 bytes, 128-
+// byte swizzle): K is a K-major operand of S = Q K^T, V an MN-major one of O = P V,
+// so V needs no transpose.  Roles:
 //   warps 0-3, 4-7   softmax of tile 0 / 1: one thread a row.  S goes from TMEM to
 //                    registers, P back over it as fp16; O is rescaled in TMEM when
-//                    m is replaced
-//   warps 8-11 (K), 13-15 (V)
-//                    cache codes to fp16: 16-byte loads of the next step's codes
-//                    are in flight while this step's are converted into
-//                    128-byte-swizzled tiles.  K and V tiles have the same
-//                    layout ([64-dim panel][key] rows of 128 bytes): K is a
-//                    K-major operand of S = Q K^T, V an MN-major one of O = P V,
-//                    so V needs no transpose
-//   warp 12          TMEM, and one thread that issues every MMA
+//                    m is replaced.  By halves of a step: P V of the first half
+//                    runs while the second is computed
+//   staged: warp 8   TMA copies;  direct: warps 8-11 (K), 13-15 (V) convert, loads
+//                    of the next step's codes in flight
+//   last / 12th      TMEM, and one elected lane that issues every MMA
 // With two tiles the tensor cores work on one while the other's softmax runs;
 // with one tile S alternates between two TMEM buffers, so that S of the next
-// step is computed during the softmax of this one.
+// step is computed during the softmax of this one.  Steps of 64 keys with two S
+// buffers for each of two tiles would take the MMAs off a tile's own chain, but
+// N = 64 score products take as long as N = 128 ones (476 us against 363).
+// Bound by the chain of a tile's step: 275 cycles to read S, 2 x 540 of softmax,
+// 150 to issue, 1130 of P V and the next S, 700 of waiting for tiles, against
+// 2112 of MMAs for both tiles: the tensor pipe is active 58% of the time (1160
+// TFLOP/s at 2048 queries, 8192 keys, 48 heads of 128).
+// Where few tiles face many keys, several CTAs share a tile's steps (Split).
 // Every wait is bounded; on expiry a role stops, what it issued is drained,
 // TMEM is freed, and bqd_device_status reports it.
 #include <cudaTypedefs.h>
@@ -842,11 +856,20 @@ int splits_of(const AttendArgs &a)
     return best;
 }
 
+// One query tile reads each code once: it converts them itself.  (Staging costs
+// five bytes of traffic a code: 8 sequences of 8000 tokens, 11 queries: 137 us.)
+template <int D>
+bool stages(const AttendArgs &a)
+{
+    return (int64_t)a.max_new * a.group > Plan<D>::kRows;
+}
+
 // Bytes of the scratch: staged tiles and their scales, then the shares
 template <int D>
 int64_t staged_bytes(const AttendArgs &a)
 {
     using P = Plan<D>;
+    if (!stages<D>(a)) return 0;
     return (int64_t)a.L.rows * a.L.heads * staged_steps<D>(a) * (2 * (int64_t)P::kKV + P::kBlocks * 8);
 }
 template <int D>
@@ -871,7 +894,10 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
     if (q_tiles * sp.count > 65535) sp.count = 1;
     const dim3 grid((unsigned)a.L.heads, (unsigned)a.L.rows, (unsigned)(q_tiles * sp.count));
     CUtensorMap map = {};
-    if (a.work) {
+    uint8_t *end = static_cast<uint8_t *>(a.work) + staged_bytes<D>(a);
+    sp.o = reinterpret_cast<float *>(end);
+    sp.ml = reinterpret_cast<float2 *>(sp.o + (int64_t)sp.count * a.tokens * a.q_heads * D);
+    if (a.work && stages<D>(a)) {
         st.steps = staged_steps<D>(a);
         const int64_t tiles = (int64_t)a.L.rows * a.L.heads * st.steps;
         st.tiles = static_cast<uint8_t *>(a.work);
@@ -885,9 +911,6 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return BQD_ERR_CUDA;
         stage_kernel<D, FMT><<<dim3(2 * st.steps, a.L.heads, a.L.rows), 256, 0, s>>>(a, st);
-        uint8_t *end = static_cast<uint8_t *>(a.work) + staged_bytes<D>(a);
-        sp.o = reinterpret_cast<float *>(end);
-        sp.ml = reinterpret_cast<float2 *>(sp.o + (int64_t)sp.count * a.tokens * a.q_heads * D);
         staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, sp, map, opt_wait_ns());
     }
     // a row can only need more steps than planned where the table's capacity does
