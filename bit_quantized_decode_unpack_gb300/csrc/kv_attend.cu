@@ -127,7 +127,8 @@ struct Tile {
 
 // The first piece of a unit that goes on in later shares
 struct Cut {
-    int row, head, ctile, last;  // last: the share with its last piece; row < 0: none
+    int lo, cols, c0, head;  // first query of its row, columns of the row and before the unit's
+    int last;                // the share with its last piece; -1: no unit is cut
 };
 
 struct Shares {
@@ -169,13 +170,13 @@ struct RowTiles {
 };
 
 template <typename T, int D>
-__device__ __forceinline__ void finish(const AttendArgs &a, const View &v, int head, int col, int d, float4 o, float mm,
-                                       float ll)
+__device__ __forceinline__ void finish(const AttendArgs &a, int lo, int cols, int c0, int head, int col, int d, float4 o,
+                                       float mm, float ll)
 {
     using H = Half2Of<T>;
-    const int c = v.c0 + col;
-    if (c >= v.cols) return;
-    const int token = v.span.lo + c / a.group, hq = head * a.group + c % a.group;
+    const int c = c0 + col;
+    if (c >= cols) return;
+    const int token = lo + c / a.group, hq = head * a.group + c % a.group;
     const float r = ll == 0.0f ? 0.0f : 1.0f / ll;
     T *at = static_cast<T *>(a.out) + ((int64_t)token * a.q_heads + hq) * D + d;
     *reinterpret_cast<uint2 *>(at) = make_uint2(H::pack(o.x * r, o.y * r), H::pack(o.z * r, o.w * r));
@@ -474,7 +475,7 @@ attend_cluster_kernel(const AttendArgs a, int S)
     float *jm = joined + TL::kWarpFloats, *jl = jm + TL::kCols;
     unit_tiles<T, D, FMT, NT>(a, v, row, head, j0, j1, smem, [&](int col, int d, float4 o, float mm, float ll) {
         if (S == 1) {
-            finish<T, D>(a, v, head, col, d, o, mm, ll);
+            finish<T, D>(a, v.span.lo, v.cols, v.c0, head, col, d, o, mm, ll);
         } else {
             *reinterpret_cast<float4 *>(joined + col * TL::kPitch + d) = o;
             if (d == 0) jm[col] = mm, jl[col] = ll;
@@ -496,7 +497,7 @@ attend_cluster_kernel(const AttendArgs a, int S)
             o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
             ll = fmaf(ld_cluster_f32(smem_addr(jl + col), r), f, ll);
         }
-        finish<T, D>(a, v, head, col, d, o, mm, ll);
+        finish<T, D>(a, v.span.lo, v.cols, v.c0, head, col, d, o, mm, ll);
     }
     cluster_sync();  // no CTA leaves while another reads its shared memory
 }
@@ -573,7 +574,7 @@ attend_shares_kernel(const AttendArgs a, const Shares sh)
         const int j1 = min(rt.lo + max(0, stop - kUnitCost), (v.hi + 15) >> 4);
         unit_tiles<T, D, FMT, NT>(a, v, row, head, j0, j1, smem, [&](int col, int d, float4 o, float mm, float ll) {
             if (starts && ends) {
-                finish<T, D>(a, v, head, col, d, o, mm, ll);
+                finish<T, D>(a, v.span.lo, v.cols, v.c0, head, col, d, o, mm, ll);
             } else {
                 *reinterpret_cast<float4 *>(piece + col * D + d) = o;
                 if (d == 0) {
@@ -584,11 +585,11 @@ attend_shares_kernel(const AttendArgs a, const Shares sh)
         });
         if (starts && !ends) {
             cut = true;
-            if (tid == 0) sh.cuts[share] = Cut{row, head, ctile, (int)((pos - j + cost - 1) / per)};
+            if (tid == 0) sh.cuts[share] = Cut{v.span.lo, v.cols, v.c0, head, (int)((pos - j + cost - 1) / per)};
         }
         pos += stop - j;
     }
-    if (!cut && tid == 0) sh.cuts[share] = Cut{-1, 0, 0, 0};
+    if (!cut && tid == 0) sh.cuts[share] = Cut{0, 0, 0, 0, -1};
     pdl_launch_dependents();
 }
 
@@ -601,27 +602,41 @@ attend_join_kernel(const AttendArgs a, const Shares sh)
     pdl_wait();
     const int share = blockIdx.x;
     const Cut cut = sh.cuts[share];
-    if (cut.row < 0) return;
-    const View v(a, cut.row, cut.ctile, TL::kCols);
     const int i = blockIdx.y * 256 + threadIdx.x, col = i / (D / 4), d = (i % (D / 4)) * 4;
-    if (col >= TL::kCols || v.c0 + col >= v.cols) return;
-    // piece 0 is what goes on, the others began earlier
-    auto piece = [&](int k) { return sh.pieces + ((int64_t)(share + k) * 2 + (k ? 0 : 1)) * TL::kPiece; };
+    if (cut.last < 0 || col >= TL::kCols || cut.c0 + col >= cut.cols) return;
+    // piece 0 is what goes on, the others began earlier; eight at a time are on their way
     const int n = cut.last - share + 1;
-    float mm = kNothing;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) mm = fmaxf(mm, piece(k)[TL::kCols * D + col]);
+    float mm = kNothing, ll = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float ll = 0.0f;
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-        const float *p = piece(k);
-        const float f = ex2(p[TL::kCols * D + col] - mm);
-        const float4 x = *reinterpret_cast<const float4 *>(p + col * D + d);
-        o.x = fmaf(x.x, f, o.x), o.y = fmaf(x.y, f, o.y), o.z = fmaf(x.z, f, o.z), o.w = fmaf(x.w, f, o.w);
-        ll = fmaf(p[TL::kCols * (D + 1) + col], f, ll);
+    constexpr int kFlight = 8;
+    for (int k0 = 0; k0 < n; k0 += kFlight) {
+        float mk[kFlight], lk[kFlight];
+        float4 x[kFlight];
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+            const int s = k0 + k;
+            mk[k] = kNothing, lk[k] = 0.0f, x[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (s < n) {
+                const float *p = sh.pieces + ((int64_t)(share + s) * 2 + (s ? 0 : 1)) * TL::kPiece;
+                mk[k] = p[TL::kCols * D + col];
+                lk[k] = p[TL::kCols * (D + 1) + col];
+                x[k] = *reinterpret_cast<const float4 *>(p + col * D + d);
+            }
+        }
+        float top = mm;
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) top = fmaxf(top, mk[k]);
+        const float r = ex2(mm - top);
+        mm = top;
+        o.x *= r, o.y *= r, o.z *= r, o.w *= r, ll *= r;
+#pragma unroll
+        for (int k = 0; k < kFlight; ++k) {
+            const float f = ex2(mk[k] - mm);
+            o.x = fmaf(x[k].x, f, o.x), o.y = fmaf(x[k].y, f, o.y), o.z = fmaf(x[k].z, f, o.z), o.w = fmaf(x[k].w, f, o.w);
+            ll = fmaf(lk[k], f, ll);
+        }
     }
-    finish<T, D>(a, v, cut.head, col, d, o, mm, ll);
+    finish<T, D>(a, cut.lo, cut.cols, cut.c0, cut.head, col, d, o, mm, ll);
 }
 
 // Makes a kernel ready on the current device, once per device.

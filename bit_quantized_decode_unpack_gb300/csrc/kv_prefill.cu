@@ -189,11 +189,12 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // query tiles in the slowest place of the grid, the last first: those see most keys, and
     // what starts last is short
-    const int head = blockIdx.x, row = blockIdx.y;
+    const unsigned pairs = (unsigned)a.L.heads * a.L.rows, place = blockIdx.x % pairs, slow = blockIdx.x / pairs;
+    const int head = place % a.L.heads, row = place / a.L.heads;
     const Span span(a.starts, row, a.tokens, a.max_new);
     const int rows = span.n * a.group;
-    const int share = blockIdx.z % sp.count;  // of the tile's steps
-    const int r0 = (int)((gridDim.z - 1 - blockIdx.z) / sp.count) * P::kRows;
+    const int share = slow % sp.count;  // of the tile's steps
+    const int r0 = (int)((gridDim.x / pairs - 1 - slow) / sp.count) * P::kRows;
     if (r0 >= rows) return;
     const int L = a.L.length(row);
     const RowSteps all_steps(L, span.n, a.window, KT);
@@ -888,11 +889,11 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
     if (!configure(direct, P::kSmem, done[0]) || !configure(staged, P::kSmem, done[1])) return BQD_ERR_CUDA;
     const int64_t rows = (int64_t)a.max_new * a.group;
     const int64_t q_tiles = (rows + P::kRows - 1) / P::kRows;
-    if (q_tiles > 65535) return BQD_ERR_INVALID_ARG;
     Staged st = {nullptr, nullptr, 0};
     Split sp = {nullptr, nullptr, a.work ? splits_of<D>(a) : 1};
-    if (q_tiles * sp.count > 65535) sp.count = 1;
-    const dim3 grid((unsigned)a.L.heads, (unsigned)a.L.rows, (unsigned)(q_tiles * sp.count));
+    const int64_t ctas = q_tiles * sp.count * a.L.heads * a.L.rows;
+    if (ctas > 0x7FFFFFFF) return BQD_ERR_INVALID_ARG;
+    const dim3 grid((unsigned)ctas);
     CUtensorMap map = {};
     uint8_t *end = static_cast<uint8_t *>(a.work) + staged_bytes<D>(a);
     sp.o = reinterpret_cast<float *>(end);
