@@ -8,7 +8,9 @@ using namespace bqd::kv;
 
 namespace {
 
-constexpr int64_t kMaxStaged = (int64_t)8 << 30;
+// scratch that a call may ask for: beyond it (a plan for very long or very many
+// rows) the codes are converted in the kernel
+constexpr int64_t kMaxStaged = (int64_t)2 << 30;
 
 bool at(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 

@@ -32,6 +32,7 @@ from . import DTYPE_BF16, DTYPE_F16, _check, load
 BLOCK = 16
 FORMATS = {"int8": 1, "e4m3": 2}
 torch = None     # bound when the first cache is made: importing the package needs no torch
+_device = _raw_stream = None  # the current device's index, a device's current stream
 _KINDS = {}      # element types of q, k and v
 PAGE_TOKENS = (16, 32, 64, 128, 256)
 HEAD_DIMS = (64, 128, 256)
@@ -64,13 +65,13 @@ def declare(lib):
 
 
 def _bind():
-    """The module's torch."""
-    global torch
+    """Binds the module's torch."""
+    global torch, _device, _raw_stream
     if torch is None:
         import torch as t
         _KINDS.update({t.float16: DTYPE_F16, t.bfloat16: DTYPE_BF16})
+        _device, _raw_stream = t.cuda.current_device, t._C._cuda_getCurrentRawStream
         torch = t
-    return torch
 
 
 def _dense(t, name, dtype, shape, device):
@@ -131,7 +132,7 @@ class KVCache:
         self.k, self.v, self.k_scales, self.v_scales = k, v, k_scales, v_scales
         self.format = kinds[k.dtype]
         self.layers, self.pages, self.kv_heads, self.page_tokens, self.head_dim = layers, pages, heads, pt, d
-        self.device, self._index = dev, dev.index
+        self.device, self._index, self._scale = dev, dev.index, 1.0 / math.sqrt(d)
         self._lib = load()
         self._attend, self._append = self._lib.bqd_kv_attend, self._lib.bqd_kv_append
         self._need = (None, 0)  # the last call's sizes and bytes of scratch
@@ -179,23 +180,23 @@ class KVCache:
 
     def _on(self, stream):
         """None, or a context that a call has to run in: another current device, or an explicit stream."""
-        if stream is None and torch.cuda.current_device() == self._index:
+        if stream is None and _device() == self._index:
             return None
         return _On(self.device, stream)
 
     def _stream(self):
-        return torch._C._cuda_getCurrentRawStream(self._index)
+        return _raw_stream(self._index)
 
     def _half(self, t, name, heads):
         """Element type of q, k or v: fp16 or bf16 [tokens, heads, head_dim] on the device, head_dim contiguous."""
-        if getattr(t, "dim", lambda: 0)() != 3 or t.device != self.device:
+        shape = getattr(t, "shape", ())
+        if len(shape) != 3 or t.device != self.device:
             raise ValueError(f"{name}: must be a 3-D tensor [tokens, heads, head_dim] on {self.device}")
         kind = _KINDS.get(t.dtype)
         if kind is None:
             raise ValueError(f"{name}: dtype {t.dtype}, expected float16 or bfloat16")
-        n, h, d = t.shape
-        if d != self.head_dim or (heads and h != heads):
-            raise ValueError(f"{name}: shape {tuple(t.shape)}, expected [tokens, {heads or 'q_heads'}, {self.head_dim}]")
+        if shape[2] != self.head_dim or (heads and shape[1] != heads):
+            raise ValueError(f"{name}: shape {tuple(shape)}, expected [tokens, {heads or 'q_heads'}, {self.head_dim}]")
         if t.stride(2) != 1:
             raise ValueError(f"{name}: head_dim must be contiguous")
         return kind
@@ -271,16 +272,15 @@ class KVCache:
         else:
             _dense(lse, "lse", torch.float32, (tokens, heads), self.device)
         # scratch, from the allocator's pool of this stream: used by this call alone
-        need = self._need
-        if need[0] != (heads, tokens, max_new, max_len, window):
-            sizes = (heads, tokens, max_new, max_len, window)
-            need = self._need = (sizes, self.attend_workspace(*sizes))
-        need = need[1]
+        sizes = (heads, tokens, max_new, max_len, window)
+        if self._need[0] != sizes:
+            self._need = (sizes, self.attend_workspace(*sizes))
+        need = self._need[1]
         work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         qs = q.stride()
         _check("bqd_kv_attend", self._attend(
             self._ref, self._layer(layer), q.data_ptr(), qs[0], qs[1], kind, heads, at, tokens, max_new, max_len,
-            1.0 / math.sqrt(d) if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
+            self._scale if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
             work.data_ptr() if need else None, need, self._stream()))
         return out, lse
 
