@@ -32,17 +32,17 @@
 //            lengths: each CTA adds them up).  What a share cuts off a unit goes
 //            to scratch, and a second kernel, launched early, joins the pieces
 //            in order.  Lengths of any mix load the GPU evenly: 32 sequences of 0
-//            to 8191 tokens 58 us with clusters, 45 us with shares.
+//            to 8191 tokens 58 us with clusters, 43 us with shares.
 //   cluster  the CTAs of a cluster split a unit's keys and join through
 //            distributed shared memory: one launch, no scratch.  For calls whose
 //            few keys would not fill the shares (latency counts), for batches of
 //            more rows than a CTA adds up, and where there is no scratch.
 // Both are free of atomics, and give the same bits every time.
 //
-// Bound by HBM for one column tile: 4 x 130001 tokens, 8 heads of 128, 168 us for
-// 1.067 GB (6361 GB/s, 95% of a measured copy; reads 1.000 of the codes).  With
+// Bound by HBM for one column tile: 4 x 130001 tokens, 8 heads of 128, 165 us for
+// 1.067 GB (6487 GB/s, 97% of a measured copy; reads 1.000 of the codes).  With
 // more columns the conversions of each pass count: two passes of 16 columns (8 x 5
-// queries) take 55 us for 116 MB, at 1.6 instructions a cycle of an SM and 12
+// queries) take 54 us for 116 MB, at 1.6 instructions a cycle of an SM and 12
 // warps of 168 registers; 32 columns a pass spill and take 73.
 #include <algorithm>
 #include <cmath>

@@ -69,6 +69,7 @@ constexpr int kThreadsStaged = (kSoftWarps + 2) * 32;  // warp 8 copies the stag
 constexpr int kStages = 2;
 constexpr int kScaleRing = 4;  // steps whose scales are kept: a slot is written again only after
                                // both softmaxes of the step four before have finished
+constexpr int64_t kMaxTiles = 65535;  // query tiles of a launch (its grid's slowest place)
 constexpr float kGrow = 15.0f;  // p stays below 2^15, inside fp16
 
 __device__ unsigned int g_prefill_timeouts = 0;
@@ -167,6 +168,7 @@ struct Split {
     float *o;       // [count][tokens * q_heads][D]
     float2 *ml;     // [count][tokens * q_heads]
     int count;      // 1: the CTA finishes its rows itself
+    int first;      // row of the launch's first query tile: a launch has 65535 tiles at most
 };
 
 template <typename T, int D, int FMT, bool STAGED>
@@ -189,12 +191,11 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // query tiles in the slowest place of the grid, the last first: those see most keys, and
     // what starts last is short
-    const unsigned pairs = (unsigned)a.L.heads * a.L.rows, place = blockIdx.x % pairs, slow = blockIdx.x / pairs;
-    const int head = place % a.L.heads, row = place / a.L.heads;
+    const int head = blockIdx.x, row = blockIdx.y;
     const Span span(a.starts, row, a.tokens, a.max_new);
     const int rows = span.n * a.group;
-    const int share = slow % sp.count;  // of the tile's steps
-    const int r0 = (int)((gridDim.x / pairs - 1 - slow) / sp.count) * P::kRows;
+    const int share = blockIdx.z % sp.count;  // of the tile's steps
+    const int r0 = (int)((gridDim.z - 1 - blockIdx.z) / sp.count) * P::kRows + sp.first;
     if (r0 >= rows) return;
     const int L = a.L.length(row);
     const RowSteps all_steps(L, span.n, a.window, KT);
@@ -890,10 +891,15 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
     const int64_t rows = (int64_t)a.max_new * a.group;
     const int64_t q_tiles = (rows + P::kRows - 1) / P::kRows;
     Staged st = {nullptr, nullptr, 0};
-    Split sp = {nullptr, nullptr, a.work ? splits_of<D>(a) : 1};
-    const int64_t ctas = q_tiles * sp.count * a.L.heads * a.L.rows;
-    if (ctas > 0x7FFFFFFF) return BQD_ERR_INVALID_ARG;
-    const dim3 grid((unsigned)ctas);
+    Split sp = {nullptr, nullptr, a.work ? splits_of<D>(a) : 1, 0};
+    if (q_tiles * sp.count > kMaxTiles) sp.count = 1;
+    // (many rows of one launch: one call of the kernels in practice)
+    auto each_launch = [&](auto launch) {
+        for (int64_t at = 0; at < q_tiles; at += kMaxTiles) {
+            sp.first = (int)(at * P::kRows);
+            launch(dim3((unsigned)a.L.heads, (unsigned)a.L.rows, (unsigned)(std::min(q_tiles - at, kMaxTiles) * sp.count)));
+        }
+    };
     CUtensorMap map = {};
     uint8_t *end = static_cast<uint8_t *>(a.work) + staged_bytes<D>(a);
     sp.o = reinterpret_cast<float *>(end);
@@ -912,11 +918,12 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
             return BQD_ERR_CUDA;
         stage_kernel<D, FMT><<<dim3(2 * st.steps, a.L.heads, a.L.rows), 256, 0, s>>>(a, st);
-        staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, sp, map, opt_wait_ns());
+        each_launch([&](dim3 grid) { staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, sp, map, opt_wait_ns()); });
     }
     // a row can only need more steps than planned where the table's capacity does
     const int64_t capacity = (int64_t)a.L.row_pages << a.L.page_shift;
-    if ((int64_t)st.steps * P::KT < capacity) direct<<<grid, kThreadsF, P::kSmem, s>>>(a, st, sp, map, opt_wait_ns());
+    if ((int64_t)st.steps * P::KT < capacity)
+        each_launch([&](dim3 grid) { direct<<<grid, kThreadsF, P::kSmem, s>>>(a, st, sp, map, opt_wait_ns()); });
     if (sp.count == 1) return cuda_status(cudaGetLastError());
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(((int64_t)a.max_new * a.q_heads * (D / 4) + 255) / 256), (unsigned)a.L.rows);
