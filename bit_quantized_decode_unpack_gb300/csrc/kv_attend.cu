@@ -148,14 +148,14 @@ struct View {
         cols = span.n * a.group;  // columns: query-major, then head of the group
         c0 = ctile * kCols;
         const int i_min = c0 / a.group, i_max = (min(c0 + kCols, cols) - 1) / a.group;
-        p_min = L - span.n + i_min;
-        p_max = L - span.n + i_max;
+        p_min = L - span.rest + i_min;
+        p_max = L - span.rest + i_max;
         hi = max(0, p_max + 1);
         lo = a.window > 0 ? max(0, p_min + 1 - a.window) : 0;
     }
 };
 
-// Tiles of a row that any of its queries sees: [lo, lo + n) (n >= 1: a row that
+// Tiles of a row that any of the call's queries sees: [lo, lo + n) (n >= 1: a row that
 // sees nothing has one, so that its zeros are written)
 struct RowTiles {
     int lo, n, ctiles;
@@ -163,8 +163,9 @@ struct RowTiles {
     {
         const Span span(a.starts, row, a.tokens, a.max_new);
         const int L = a.L.length(row);
-        lo = a.window > 0 ? max(0, L - span.n + 1 - a.window) >> 4 : 0;
-        n = max(1, ((L + 15) >> 4) - lo);
+        const int first = L - span.rest;  // position of query 0
+        lo = a.window > 0 ? max(0, first + 1 - a.window) >> 4 : 0;
+        n = max(1, ((max(0, first + span.n) + 15) >> 4) - lo);
         ctiles = (span.n * a.group + kCols - 1) / kCols;
     }
 };
@@ -297,7 +298,7 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_,
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int cc = c0 + n * 8 + 2 * t + h;
-            pos[n][h] = cc < cols ? L - span.n + cc / a.group : -1;
+            pos[n][h] = cc < cols ? L - span.rest + cc / a.group : -1;
         }
     }
 

@@ -44,17 +44,22 @@ struct Layer {
     }
 };
 
-// Tokens [lo, hi) of row r among T: starts[r] .. starts[r + 1], or token r.
+// Tokens [lo, lo + n) of row r among T that the call takes: starts[r] .. starts[r + 1],
+// or token r, cut to T and to max_new of them.  `rest` counts the tokens from lo to
+// the row's end as starts gives it: token lo + i is the (rest - i)-th from the end,
+// whatever the cuts left out.
 struct Span {
-    int lo, n;
+    int lo, n, rest;
     __device__ __forceinline__ Span(const int32_t *starts, int row, int tokens, int max_new)
     {
         if (starts) {
             lo = max(0, min(starts[row], tokens));
-            n = min(max(0, min(starts[row + 1], tokens) - lo), max_new);
+            const int end = starts[row + 1];
+            n = min(max(0, min(end, tokens) - lo), max_new);
+            rest = n > 0 ? min(end - lo, 1 << 30) : 0;  // (a row has no more tokens than a call may)
         } else {
             lo = row;
-            n = 1;
+            n = rest = 1;
         }
     }
 };

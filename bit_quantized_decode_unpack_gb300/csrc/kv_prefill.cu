@@ -144,13 +144,14 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Keys [lo, lo + steps * KT) of a row that any of its n queries sees.
+// Keys [lo, lo + steps * KT) of a row of length L that any of the call's queries sees.
 struct RowSteps {
     int lo, steps;
-    __device__ __forceinline__ RowSteps(int L, int n, int window, int KT)
+    __device__ __forceinline__ RowSteps(int L, const Span &span, int window, int KT)
     {
-        lo = window > 0 ? max(0, L - n + 1 - window) / KT * KT : 0;
-        steps = n > 0 && L > lo ? (L - lo + KT - 1) / KT : 0;
+        const int first = L - span.rest, hi = max(0, first + span.n);  // position of query 0, end of the keys
+        lo = window > 0 ? max(0, first + 1 - window) / KT * KT : 0;
+        steps = span.n > 0 && hi > lo ? (hi - lo + KT - 1) / KT : 0;
     }
 };
 
@@ -198,12 +199,12 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
     const int r0 = (int)((gridDim.z - 1 - blockIdx.z) / sp.count) * P::kRows + sp.first;
     if (r0 >= rows) return;
     const int L = a.L.length(row);
-    const RowSteps all_steps(L, span.n, a.window, KT);
+    const RowSteps all_steps(L, span, a.window, KT);
     // rows that the scratch has no room for are the unstaged form's
     if (st.steps > 0 && (all_steps.steps <= st.steps) != STAGED) return;
     const int tiles = min(P::kTiles, (rows - r0 + 127) / 128);
     const int i_min = r0 / a.group, i_max = (min(r0 + P::kRows, rows) - 1) / a.group;
-    const int p_first = L - span.n;  // position of query 0
+    const int p_first = L - span.rest;  // position of query 0
     const int hi = max(0, p_first + i_max + 1);
     const int lo = a.window > 0 ? max(0, p_first + i_min + 1 - a.window) : 0;
     const int k_first = lo / KT * KT, all = hi > k_first ? (hi - k_first + KT - 1) / KT : 0;
@@ -765,7 +766,7 @@ stage_kernel(const AttendArgs a, const Staged st)
     const int j = blockIdx.x >> 1, which = blockIdx.x & 1, head = blockIdx.y, row = blockIdx.z;
     const Span span(a.starts, row, a.tokens, a.max_new);
     const int L = a.L.length(row);
-    const RowSteps all(L, span.n, a.window, KT);
+    const RowSteps all(L, span, a.window, KT);
     if (j >= all.steps || all.steps > st.steps) return;
     const int k0 = all.lo + j * KT;
     const int64_t step = ((int64_t)row * a.L.heads + head) * st.steps + j;

@@ -294,9 +294,11 @@ int bqd_kv_append(const bqd_kv_cache *cache, int layer, const void *k, int64_t k
  *   out     device [tokens, q_heads, head_dim] of `dtype`, dense, 16-byte
  *           aligned; rows of q outside every row's range are left as they are
  *   lse     device fp32 [tokens, q_heads] or NULL
- *   max_new an upper bound of starts[r+1] - starts[r] (later queries of a row
- *           are not computed); max_len a bound of lens that the launch is
- *           planned for (0: the table's capacity); longer rows stay correct
+ *   max_new an upper bound of starts[r+1] - starts[r].  A row's later queries,
+ *           and those past `tokens`, are not computed; the others keep the
+ *           positions that the row's true count n gives them
+ *   max_len a bound of lens that the launch is planned for (0: the table's
+ *           capacity); longer rows stay correct
  *   scale   finite;  window >= 0 (0: none)
  *   work    device scratch, 16-byte aligned, of work_bytes bytes, or NULL with
  *           0.  bqd_kv_attend_workspace (host-only) gives the bytes that a
