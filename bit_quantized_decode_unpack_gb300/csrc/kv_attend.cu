@@ -155,7 +155,7 @@ struct View {
     }
 };
 
-// Tiles of a row that any of the call's queries sees: [lo, lo + n) (n >= 1: a row that
+// Tiles of a row that any of its queries sees: [lo, lo + n) (n >= 1: a row that
 // sees nothing has one, so that its zeros are written)
 struct RowTiles {
     int lo, n, ctiles;
@@ -163,9 +163,8 @@ struct RowTiles {
     {
         const Span span(a.starts, row, a.tokens, a.max_new);
         const int L = a.L.length(row);
-        const int first = L - span.rest;  // position of query 0
-        lo = a.window > 0 ? max(0, first + 1 - a.window) >> 4 : 0;
-        n = max(1, ((max(0, first + span.n) + 15) >> 4) - lo);
+        lo = a.window > 0 ? max(0, L - span.rest + 1 - a.window) >> 4 : 0;
+        n = max(1, ((L + 15) >> 4) - lo);
         ctiles = (span.n * a.group + kCols - 1) / kCols;
     }
 };

@@ -56,7 +56,7 @@ struct Span {
             lo = max(0, min(starts[row], tokens));
             const int end = starts[row + 1];
             n = min(max(0, min(end, tokens) - lo), max_new);
-            rest = n > 0 ? min(end - lo, 1 << 30) : 0;  // (a row has no more tokens than a call may)
+            rest = min(max(end, lo) - lo, 1 << 30);  // (a row has no more tokens than a call may)
         } else {
             lo = row;
             n = rest = 1;

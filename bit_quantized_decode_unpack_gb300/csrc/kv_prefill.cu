@@ -144,14 +144,13 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Keys [lo, lo + steps * KT) of a row of length L that any of the call's queries sees.
+// Keys [lo, lo + steps * KT) of a row of length L that any of its queries sees.
 struct RowSteps {
     int lo, steps;
     __device__ __forceinline__ RowSteps(int L, const Span &span, int window, int KT)
     {
-        const int first = L - span.rest, hi = max(0, first + span.n);  // position of query 0, end of the keys
-        lo = window > 0 ? max(0, first + 1 - window) / KT * KT : 0;
-        steps = span.n > 0 && hi > lo ? (hi - lo + KT - 1) / KT : 0;
+        lo = window > 0 ? max(0, L - span.rest + 1 - window) / KT * KT : 0;
+        steps = span.n > 0 && L > lo ? (L - lo + KT - 1) / KT : 0;
     }
 };
 
