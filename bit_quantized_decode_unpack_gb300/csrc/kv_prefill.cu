@@ -709,12 +709,15 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                 if (!next) commit(o_full(0));
             }
         }
-        if (!ok && steps > 0) {
-            // what was issued reads and writes this CTA's memory: let it finish
+        if (steps > 0) {
+            // On every exit, since another role's wait may have run out although none of this one's
+            // did: what was issued reads shared memory, writes TMEM and arrives on barriers of this
+            // CTA.  Let it finish.
             commit(drained);
             mbar_wait_for(drained, 0, kDrainWaitNs, &g_prefill_timeouts);
         }
     }
+    st_wait();  // a role that gave up may have stores to TMEM on their way
     fence_before();
     __syncthreads();
     fence_after();
