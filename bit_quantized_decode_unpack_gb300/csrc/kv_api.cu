@@ -8,10 +8,6 @@ using namespace bqd::kv;
 
 namespace {
 
-// scratch that a call may ask for: beyond it (a plan for very long or very many
-// rows) the codes are converted in the kernel
-constexpr int64_t kMaxStaged = (int64_t)2 << 30;
-
 bool at(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // Status of a cache's sizes and pointers.  A cache of no rows needs no table.
@@ -98,12 +94,7 @@ int planned_length(const bqd_kv_cache &c, int64_t max_len)
 bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 32 : 48); }
 
 // bytes of scratch that a call is better with, or 0
-int64_t scratch_need(const AttendArgs &a)
-{
-    if (!many_queries(a)) return decode_workspace(a);
-    const int64_t bytes = prefill_workspace(a);
-    return bytes <= kMaxStaged ? bytes : 0;
-}
+int64_t scratch_need(const AttendArgs &a) { return many_queries(a) ? prefill_workspace(a) : decode_workspace(a); }
 
 cudaStream_t to_stream(bqd_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 

@@ -70,6 +70,7 @@ constexpr int kStages = 2;
 constexpr int kScaleRing = 4;  // steps whose scales are kept: a slot is written again only after
                                // both softmaxes of the step four before have finished
 constexpr int64_t kMaxTiles = 65535;  // query tiles of a launch (its grid's slowest place)
+constexpr int64_t kMaxScratch = (int64_t)2 << 30;  // bytes that a call may ask for
 constexpr float kGrow = 15.0f;  // p stays below 2^15, inside fp16
 
 __device__ unsigned int g_prefill_timeouts = 0;
@@ -144,13 +145,16 @@ __device__ __forceinline__ float ex2(float x)
     return y;
 }
 
-// Keys [lo, lo + steps * KT) of a row of length L that any of its queries sees.
+// Keys [lo, lo + steps * KT) of a row of length L that any of its queries sees; with a window, that any
+// of the call's queries sees (without one the end stays the row's, so that nothing waits for `starts`).
 struct RowSteps {
     int lo, steps;
     __device__ __forceinline__ RowSteps(int L, const Span &span, int window, int KT)
     {
-        lo = window > 0 ? max(0, L - span.rest + 1 - window) / KT * KT : 0;
+        const int first = L - span.rest;  // position of query 0
+        lo = window > 0 ? max(0, first + 1 - window) / KT * KT : 0;
         steps = span.n > 0 && L > lo ? (L - lo + KT - 1) / KT : 0;
+        if (window > 0) steps = min(steps, max(0, first + span.n - lo + KT - 1) / KT);
     }
 };
 
@@ -832,12 +836,28 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
     return fn;
 }
 
-// Steps of a row that the scratch is laid out for, and its bytes
+// Keys that a row of length `len` at most can need: a window and its queries hide the others
+int64_t keys_of(const AttendArgs &a, int64_t len)
+{
+    return a.window > 0 ? std::min<int64_t>(len, (int64_t)a.window + a.max_new) : len;
+}
+
+// Steps of a row that the scratch is laid out for
 template <int D>
 int staged_steps(const AttendArgs &a)
 {
-    return a.max_len / Plan<D>::KT + 2;  // a window's first step may start before its keys
+    return (int)(keys_of(a, a.max_len) / Plan<D>::KT) + 2;  // a window's first step may start before its keys
 }
+
+// Steps that a row can need at most, whatever its length
+template <int D>
+int64_t most_steps(const AttendArgs &a)
+{
+    constexpr int KT = Plan<D>::KT;
+    const int64_t capacity = (int64_t)a.L.row_pages << a.L.page_shift, all = (capacity + KT - 1) / KT;
+    return std::min(all, keys_of(a, capacity) / KT + 2);
+}
+
 // CTAs that share a query tile's steps: the count with the least time, in steps
 // of a full tile, over the waves of CTAs (one an SM).  A CTA costs about three
 // steps to begin and end, and to leave and join its O three and a half more
@@ -849,8 +869,7 @@ int splits_of(const AttendArgs &a)
     using P = Plan<D>;
     const int64_t rows = (int64_t)a.max_new * a.group;
     const int64_t ctas = (rows + P::kRows - 1) / P::kRows * a.L.heads * a.L.rows;
-    const int64_t span = a.window > 0 ? std::min<int64_t>(a.max_len, (int64_t)a.window + a.max_new) : a.max_len;
-    const double steps = (double)(span + P::KT - 1) / P::KT;
+    const double steps = (double)(keys_of(a, a.max_len) + P::KT - 1) / P::KT;
     const int sms = sm_count();
     int best = 1;
     double least = 1e30;
@@ -869,19 +888,28 @@ bool stages(const AttendArgs &a)
     return (int64_t)a.max_new * a.group > Plan<D>::kRows;
 }
 
-// Bytes of the scratch: staged tiles and their scales, then the shares
+// The scratch: staged tiles and their scales, then the shares.  A plan for very long or very many rows
+// goes without the tiles (the codes are converted in the kernel), and without shares only where those
+// alone are too many.
 template <int D>
-int64_t staged_bytes(const AttendArgs &a)
-{
-    using P = Plan<D>;
-    if (!stages<D>(a)) return 0;
-    return (int64_t)a.L.rows * a.L.heads * staged_steps<D>(a) * (2 * (int64_t)P::kKV + P::kBlocks * 8);
-}
-template <int D>
-int64_t split_bytes(const AttendArgs &a, int splits)
-{
-    return splits > 1 ? (int64_t)splits * a.tokens * a.q_heads * (D * 4 + 8) : 0;
-}
+struct Scratch {
+    int steps = 0, splits = 1;  // staged steps of a row (0: none), CTAs that share a query tile's steps
+    int64_t staged = 0, bytes = 0;
+    explicit Scratch(const AttendArgs &a)
+    {
+        using P = Plan<D>;
+        if (stages<D>(a)) {
+            steps = staged_steps<D>(a);
+            staged = (int64_t)a.L.rows * a.L.heads * steps * (2 * (int64_t)P::kKV + P::kBlocks * 8);
+            if (staged > kMaxScratch) steps = 0, staged = 0;
+        }
+        bytes = staged;
+        const int n = splits_of<D>(a);
+        const int64_t q_tiles = ((int64_t)a.max_new * a.group + P::kRows - 1) / P::kRows;
+        const int64_t shares = (int64_t)n * a.tokens * a.q_heads * (D * 4 + 8);
+        if (n > 1 && q_tiles * n <= kMaxTiles && staged + shares <= kMaxScratch) splits = n, bytes += shares;
+    }
+};
 
 template <typename T, int D, int FMT>
 int launch_t(const AttendArgs &a, cudaStream_t s)
@@ -893,9 +921,9 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
     if (!configure(direct, P::kSmem, done[0]) || !configure(staged, P::kSmem, done[1])) return BQD_ERR_CUDA;
     const int64_t rows = (int64_t)a.max_new * a.group;
     const int64_t q_tiles = (rows + P::kRows - 1) / P::kRows;
-    Staged st = {nullptr, nullptr, 0};
-    Split sp = {nullptr, nullptr, a.work ? splits_of<D>(a) : 1, 0};
-    if (q_tiles * sp.count > kMaxTiles) sp.count = 1;
+    const Scratch<D> plan(a);
+    Staged st = {nullptr, nullptr, a.work ? plan.steps : 0};
+    Split sp = {nullptr, nullptr, a.work ? plan.splits : 1, 0};
     // (many rows of one launch: one call of the kernels in practice)
     auto each_launch = [&](auto launch) {
         for (int64_t at = 0; at < q_tiles; at += kMaxTiles) {
@@ -904,11 +932,10 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
         }
     };
     CUtensorMap map = {};
-    uint8_t *end = static_cast<uint8_t *>(a.work) + staged_bytes<D>(a);
+    uint8_t *end = static_cast<uint8_t *>(a.work) + plan.staged;
     sp.o = reinterpret_cast<float *>(end);
     sp.ml = reinterpret_cast<float2 *>(sp.o + (int64_t)sp.count * a.tokens * a.q_heads * D);
-    if (a.work && stages<D>(a)) {
-        st.steps = staged_steps<D>(a);
+    if (st.steps > 0) {
         const int64_t tiles = (int64_t)a.L.rows * a.L.heads * st.steps;
         st.tiles = static_cast<uint8_t *>(a.work);
         st.scales = reinterpret_cast<float2 *>(st.tiles + tiles * 2 * P::kKV);
@@ -923,9 +950,7 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
         stage_kernel<D, FMT><<<dim3(2 * st.steps, a.L.heads, a.L.rows), 256, 0, s>>>(a, st);
         each_launch([&](dim3 grid) { staged<<<grid, kThreadsStaged, P::kSmem, s>>>(a, st, sp, map, opt_wait_ns()); });
     }
-    // a row can only need more steps than planned where the table's capacity does
-    const int64_t capacity = (int64_t)a.L.row_pages << a.L.page_shift;
-    if ((int64_t)st.steps * P::KT < capacity)
+    if (most_steps<D>(a) > st.steps)  // rows that need more steps than planned, or all of them
         each_launch([&](dim3 grid) { direct<<<grid, kThreadsF, P::kSmem, s>>>(a, st, sp, map, opt_wait_ns()); });
     if (sp.count == 1) return cuda_status(cudaGetLastError());
     cudaLaunchConfig_t cfg = {};
@@ -955,7 +980,7 @@ int64_t prefill_workspace(const AttendArgs &a)
 {
     auto bytes = [&](auto d) {
         constexpr int D = decltype(d)::value;
-        return staged_bytes<D>(a) + split_bytes<D>(a, splits_of<D>(a));
+        return Scratch<D>(a).bytes;
     };
     return a.head_dim == 64    ? bytes(std::integral_constant<int, 64>())
            : a.head_dim == 128 ? bytes(std::integral_constant<int, 128>())
