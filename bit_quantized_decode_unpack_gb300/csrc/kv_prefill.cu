@@ -527,6 +527,7 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
         // that no load's address waits for another load.  Lane b < KT / 16 keeps the place of
         // the step's block b; the others get it by shuffle.
         constexpr int kItems = P::kPanels * KT / 8;
+        const int end = min(hi, k_lo + steps * KT);  // of this CTA's keys
         const int part = lane & 3, sub = lane >> 2;
         auto convert = [&](auto warps, int cw, const uint8_t *pool, uint32_t tile0, auto full, auto empty, bool is_k) {
             constexpr int kW = decltype(warps)::value, kEach = (kItems + kW - 1) / kW;
@@ -537,7 +538,7 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
             float ksc = 1.0f, vsc = 1.0f;
             auto look_up = [&](int j) {
                 const int t = k_lo + j * KT + lane * kBlock;
-                page = lane < P::kBlocks && t < hi ? a.L.listed(row, t) : 0;
+                page = lane < P::kBlocks && t < end ? a.L.listed(row, t) : 0;
             };
             auto load = [&](int j) {
                 const int k0 = k_lo + j * KT;
@@ -551,10 +552,10 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                     // keys past the last that is seen: 0, never stale bytes
                     x[i] = ld_stream_v4_if(
                         pool + b * (kBlock * D) + ((eight & 1) * 8 + sub) * D + item / (KT / 8) * 64 + part * 16,
-                        item < kItems && k0 + eight * 8 + sub < hi);
+                        item < kItems && k0 + eight * 8 + sub < end);
                 }
                 ksc = vsc = 1.0f;
-                if (scaler && lane < P::kBlocks && k0 + lane * kBlock < hi) {
+                if (scaler && lane < P::kBlocks && k0 + lane * kBlock < end) {
                     ksc = __ldg(a.L.ks + place);
                     vsc = __ldg(a.L.vs + place);
                 }
