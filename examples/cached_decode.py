@@ -84,9 +84,10 @@ class Decoder(torch.nn.Module):
 def generate(model, prompts, new_tokens, drafts=4, draft=None, **cache_kw):
     """Continues each prompt (a list of token ids) greedily by at least new_tokens tokens.
 
-    ``draft(row, sequence, n)`` guesses n tokens (default: repeats the last one); whatever it
-    guesses, the tokens are those that the model takes by itself.  Returns (sequences, cache,
-    accepted drafts)."""
+    ``draft(row, sequence, n)`` guesses n tokens (default: repeats the last one); every token taken is
+    the model's own choice after those before it.  (A rejected guess leaves the cache, but may have
+    raised its block's scale: two runs with other guesses agree as far as 8 bits do.)  A row leaves
+    the batch with the step that reaches its goal.  Returns (sequences, cache, accepted drafts)."""
     draft = draft or (lambda row, seq, n: [seq[-1]] * n)
     rows, longest = len(prompts), max(map(len, prompts)) + new_tokens + drafts + 1
     pt = cache_kw.get("page_tokens", 64)
@@ -97,17 +98,16 @@ def generate(model, prompts, new_tokens, drafts=4, draft=None, **cache_kw):
     model(torch.tensor(sum(heads, []), device="cuda"), [len(h) for h in heads], cache, longest)
     goal = [len(p) + new_tokens for p in prompts]
     hits = 0
-    while any(len(s) < g for s, g in zip(seqs, goal)):
-        guesses = [draft(r, s, drafts) for r, s in enumerate(seqs)]
-        tokens = torch.tensor([[s[-1]] + g for s, g in zip(seqs, guesses)], device="cuda")
-        logits = model(tokens.view(-1), [1 + drafts] * rows, cache, longest)
+    while live := [r for r in range(rows) if len(seqs[r]) < goal[r]]:
+        guesses = [draft(r, seqs[r], drafts) for r in live]
+        tokens = torch.tensor([[seqs[r][-1]] + g for r, g in zip(live, guesses)], device="cuda")
+        counts = [1 + drafts if r in live else 0 for r in range(rows)]
+        logits = model(tokens.view(-1), counts, cache, longest)
         accepted, following = bqd.spec_decode_verify(
-            logits.view(rows, 1 + drafts, -1), tokens[:, 1:].to(torch.int32).contiguous())
-        accepted, following = accepted.tolist(), following.tolist()
-        for r in range(rows):
-            if len(seqs[r]) < goal[r]:
-                seqs[r] += guesses[r][:accepted[r]] + [following[r]]
-                hits += accepted[r]
+            logits.view(len(live), 1 + drafts, -1), tokens[:, 1:].to(torch.int32).contiguous())
+        for r, g, n, token in zip(live, guesses, accepted.tolist(), following.tolist()):
+            seqs[r] += g[:n] + [token]
+            hits += n
         # the cache holds every token but the newest of each sequence
         cache = cache.truncate(torch.tensor([len(s) - 1 for s in seqs], dtype=torch.int32, device="cuda"))
     return seqs, cache, hits
