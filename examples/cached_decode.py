@@ -95,7 +95,8 @@ def generate(model, prompts, new_tokens, drafts=4, draft=None, **cache_kw):
     seqs = [list(p) for p in prompts]
     # the prompts, but for their last tokens: each step starts with the newest token of a sequence
     heads = [p[:-1] for p in prompts]
-    model(torch.tensor(sum(heads, []), device="cuda"), [len(h) for h in heads], cache, longest)
+    if any(heads):
+        model(torch.tensor(sum(heads, []), device="cuda"), [len(h) for h in heads], cache, longest)
     goal = [len(p) + new_tokens for p in prompts]
     hits = 0
     while live := [r for r in range(rows) if len(seqs[r]) < goal[r]]:

@@ -64,6 +64,14 @@ def test_a_row_that_ends_early_and_past_its_goal(example, page_tokens, lengths, 
     assert int((cache.refs > 0).sum()) == sum(-(-(len(s) - 1) // page_tokens) for s in seqs)
 
 
+@pytest.mark.parametrize("lengths", [(1,), (1, 1, 1), (1, 30)])
+def test_prompts_of_one_token(example, lengths):
+    model, prompts = example.Decoder(), _prompts(*lengths)
+    seqs, cache, _ = example.generate(model, prompts, 6, drafts=2, page_tokens=16)
+    assert all(len(s) >= len(p) + 6 for s, p in zip(seqs, prompts))
+    assert cache.lens.tolist() == [len(s) - 1 for s in seqs]
+
+
 @pytest.mark.parametrize("new", [1, 2, 9, 24])
 def test_after_rejected_drafts_the_cache_holds_the_same_tokens(example, new):
     import torch
