@@ -123,7 +123,7 @@ extern "C" int bqd_kv_append(const bqd_kv_cache *cache, int layer, const void *k
     a.head_stride[0] = k_head_stride, a.head_stride[1] = v_head_stride;
     a.base = base, a.starts = starts;
     a.dtype = dtype, a.format = c.format, a.head_dim = c.head_dim;
-    a.tokens = (int)tokens, a.max_new = starts ? (int)max_new : 1;
+    a.tokens = (int)tokens, a.max_new = starts ? (int)(max_new < tokens ? max_new : tokens) : 1;
     a.vec = vec_ok(k, k_token_stride, k_head_stride) && vec_ok(v, v_token_stride, v_head_stride);
     return launch_append(a, to_stream(stream));
 }
