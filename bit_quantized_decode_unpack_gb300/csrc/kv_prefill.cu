@@ -26,8 +26,8 @@
 // so V needs no transpose.  Roles:
 //   warps 0-3, 4-7   softmax of tile 0 / 1: one thread a row.  S goes from TMEM to
 //                    registers, P back over it as fp16; O is rescaled in TMEM when
-//                    m is replaced.  By halves of a step: P V of the first half
-//                    runs while the second is computed
+//                    m is replaced.  By halves of a step (head_dim 256: whole
+//                    steps): P V of the first half runs while the second is computed
 //   staged: warp 8   TMA copies;  direct: warps 8-11 (K), 13-15 (V) convert, loads
 //                    of the next step's codes in flight
 //   last / 12th      TMEM, and one elected lane that issues every MMA
@@ -87,6 +87,11 @@ struct Plan {
     static constexpr uint32_t kKV = kPanels * kPanelKV;  // one K or V tile
     static constexpr uint32_t kOffK = kQ, kOffV = kOffK + kStages * kKV, kOffEnd = kOffV + kStages * kKV;
     static constexpr int kBlocks = KT / kBlock;
+    // Parts of a step's softmax.  One tile's step of 64 keys is one part, its maximum found before the
+    // exponentials: nothing hides a part's latency, and 32 columns are too few to do so by themselves
+    // (2048 queries at 8192 keys: 361 us in halves, 340 in one part with the maximum beside the
+    // exponentials, 326 so).
+    static constexpr int kParts = kTiles == 1 ? 1 : 2;
     static constexpr size_t kSmem = 1024 + kOffEnd;
     // TMEM columns
     static constexpr uint32_t kS1 = KT, kO0 = 256, kO1 = 256 + D, kCols = 512;
@@ -357,17 +362,30 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                 const int k0 = k_lo + j * KT;
                 const bool whole = k0 + KT - 1 <= p_low && (a.window == 0 || k0 > p_high - a.window);
                 const int last = pos - k0, first = a.window > 0 ? last - a.window : -1;  // seen: first < i <= last
-                // Half of the step's columns at a time: the MMAs of the first half's P run while the
-                // second half is computed.  Exponentials are taken against the reference that is
-                // there, with the half's maximum found beside them; where a row passes its reference
-                // by too much (the first step, seldom after it) the warp replaces it and computes
-                // the half again.  P takes the place of scores that were read, two values a column.
-                constexpr int kHalf = KT / 2, kHalfBlocks = kHalf / 16, kChunks = kHalf / 32;
-                uint32_t s[2][kChunks][32];
+                // Half of the step's columns at a time (but see kParts): the MMAs of the first half's P
+                // run while the second half is computed.  Exponentials are taken against the reference
+                // that is there, with the half's maximum found beside them; where a row passes its
+                // reference by too much (the first step, seldom after it) the warp replaces it and
+                // computes the half again.  P takes the place of scores that were read, two values a
+                // column.
+                constexpr int kHalf = KT / P::kParts, kHalfBlocks = kHalf / 16, kChunks = kHalf / 32;
+                uint32_t s[P::kParts][kChunks][32];
 #pragma unroll
                 for (int c = 0; c < kChunks; ++c) ld32(s_at + 32 * c, s[0][c]);
+                auto rescale = [&](float f) {  // O times f
+                    fence_after();
+#pragma unroll 1
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t o[16];
+                        ld16(o_at + 16 * k, o);
+                        ld_wait(o);
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                        for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                        st16(o_at + 16 * k, o);
+                    }
+                };
+#pragma unroll
+                for (int half = 0; half < P::kParts; ++half) {
                     const float2 *v = sc + half * kHalfBlocks;
                     uint32_t (&sh)[kChunks][32] = s[half];
                     if (half == 1) {
@@ -380,6 +398,29 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
 #pragma unroll
                         for (int i = 0; i < kHalf; ++i)
                             if (half * kHalf + i > last || half * kHalf + i <= first) sh[i / 32][i % 32] = 0xFF800000u;  // -inf
+                    }
+                    if constexpr (P::kParts == 1) {
+                        float mt = -INFINITY;
+#pragma unroll
+                        for (int b = 0; b < kHalfBlocks; ++b) {
+                            const uint32_t *x = &sh[b / 2][16 * (b & 1)];
+                            float top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+#pragma unroll
+                            for (int i = 2; i < 16; i += 2)
+                                top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                            mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
+                        }
+                        if (__any_sync(0xffffffffu, mt > m + kGrow)) {
+                            const float mn = mt > m + kGrow ? mt : m;
+                            const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+                            m = mn;
+                            l *= f;
+                            if (j > 0) {
+                                ok = __all_sync(0xffffffffu, wait(pv_done, j - 1));  // it still adds to O
+                                if (!ok) break;
+                                rescale(f);
+                            }
+                        }
                     }
                     float sum;
                     while (true) {
@@ -403,12 +444,12 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                                 part = add2(part, two(e0, e1));
                                 p[i / 2] = Half2Of<__half>::pack(e0, e1);
                             }
-                            mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
+                            if (P::kParts > 1) mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
                             const float2 t = untwo(part);
                             sum = fmaf(t.x + t.y, ex2(-v[b].y), sum);
                             st8(s_at + half * (kHalf / 2) + 8 * b, p);
                         }
-                        if (!__any_sync(0xffffffffu, mt > m + kGrow)) break;
+                        if (P::kParts == 1 || !__any_sync(0xffffffffu, mt > m + kGrow)) break;
                         const float mn = mt > m + kGrow ? mt : m;
                         const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
                         m = mn;
@@ -420,16 +461,7 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                             if (ok && half) ok = wait(pv_half(w), j);
                             ok = __all_sync(0xffffffffu, ok);
                             if (!ok) break;
-                            fence_after();
-#pragma unroll 1
-                            for (int k = 0; k < D / 16; ++k) {
-                                uint32_t o[16];
-                                ld16(o_at + 16 * k, o);
-                                ld_wait(o);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                                st16(o_at + 16 * k, o);
-                            }
+                            rescale(f);
                         }
                     }
                     if (!ok) break;
@@ -646,12 +678,12 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
         auto pv = [&](int j, int w, int slot, int half) {
             const uint32_t v = v_lo + (j % kStages) * (P::kKV / 16);
 #pragma unroll
-            for (int i = 0; i < KT / 32; ++i) {
-                const int s = half * (KT / 32) + i;
+            for (int i = 0; i < KT / (16 * P::kParts); ++i) {
+                const int s = half * (KT / (16 * P::kParts)) + i;
                 mma_ts(tmem + (w ? P::kO1 : P::kO0), tmem + (slot ? P::kS1 : 0) + 8 * s, v + s * (16 * 128 / 16), hi_word,
                        i_pv, j > 0 || s > 0);
             }
-            if (!half) commit(pv_half(w));
+            if (half + 1 < P::kParts) commit(pv_half(w));
         };
         // What ordinary stores wrote (Q, and the tiles of the direct form) is read by the MMAs: the
         // fence between the two stands here, after the wait, because the writers have loads in
@@ -661,8 +693,8 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
             if (!STAGED) fence_proxy_async_smem();
         };
         auto all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
-        auto both = [&](int j, int w, int slot, int parity) {  // O += P V of a step, by halves
-            for (int half = 0; half < 2; ++half) {
+        auto both = [&](int j, int w, int slot, int parity) {  // O += P V of a step, by parts
+            for (int half = 0; half < P::kParts; ++half) {
                 if (!all(p_full(slot, half), parity)) return false;
                 fence_after();
                 pv(j, w, slot, half);
