@@ -88,9 +88,9 @@ int planned_length(const bqd_kv_cache &c, int64_t max_len)
 
 // Queries enough for 128-row tiles on tcgen05.  The other kernel reads the keys
 // once for each 16 (query, head) columns (8 with head_dim 256).  Measured with 8
-// sequences of 8000 tokens, head_dim 64 / 128, it takes 54 / 86 us at 48 columns and
-// 65 / 119 at 54; the tiles 64 / 102 at any.  With head_dim 256 it takes 73 us at 24
-// columns, 93 at 30 and 113 at 36, the tiles 86; with one sequence 17, 19 and 20
+// sequences of 8000 tokens, head_dim 64 / 128, it takes 53 / 86 us at 48 columns and
+// 65 / 118 at 54; the tiles 56 / 81 at any.  With head_dim 256 it takes 73 us at 24
+// columns, 93 at 30 and 113 at 36, the tiles 83; with one sequence 17, 19 and 20
 // against 29 to 31.
 bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 32 : 48); }
 

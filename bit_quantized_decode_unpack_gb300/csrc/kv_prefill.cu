@@ -20,14 +20,14 @@
 //   direct   seven warps convert the codes in the kernel: for one query tile a
 //            row, calls without scratch, and rows longer than planned.  Their
 //            code and the softmax's share the instruction cache and the issue
-//            slots: 2048 queries at 8192 keys take 311 us staged, 545 direct.
+//            slots: 2048 queries at 8192 keys take 311 us staged, 473 direct.
 // K and V tiles have the same layout ([64-dim panel][key] rows of 128 bytes, 128-
 // byte swizzle): K is a K-major operand of S = Q K^T, V an MN-major one of O = P V,
 // so V needs no transpose.  Roles:
 //   warps 0-3, 4-7   softmax of tile 0 / 1: one thread a row.  S goes from TMEM to
 //                    registers, P back over it as fp16; O is rescaled in TMEM when
-//                    m is replaced.  By halves of a step (head_dim 256: whole
-//                    steps): P V of the first half runs while the second is computed
+//                    m is replaced.  Staged: by halves of a step (head_dim 256: whole
+//                    steps), so that P V of the first runs while the second is computed
 //   staged: warp 8   TMA copies;  direct: warps 8-11 (K), 13-15 (V) convert, loads
 //                    of the next step's codes in flight
 //   last / 12th      TMEM, and one elected lane that issues every MMA
@@ -191,6 +191,7 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
     constexpr int kFillersK = STAGED ? 1 : kWarpsK, kFillersV = STAGED ? 1 : kWarpsV;
     using H = Half2Of<T>;
     constexpr int KT = P::KT;
+    constexpr int kParts = STAGED ? P::kParts : 1;  // of a step's softmax
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t bars[4 * kStages + 13 + kScaleRing];
     __shared__ __align__(16) float2 scales[kScaleRing][8];  // of a step's blocks: K's scale, log2 of V's
@@ -350,11 +351,13 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                 // the blocks' scales while S is on its way: shared memory answers slowly (300 to 400
                 // cycles) while the MMAs read their operands from it
                 ok = wait(sc_full(j), j / kScaleRing);
-                float2 sc[P::kBlocks];
+                float2 sr[P::kBlocks];
+                if constexpr (STAGED) {
 #pragma unroll
-                for (int b = 0; b < P::kBlocks; ++b) {
-                    sc[b] = scales[j % kScaleRing][b];
-                    sc[b].x = factor(sc[b].x);
+                    for (int b = 0; b < P::kBlocks; ++b) {
+                        sr[b] = scales[j % kScaleRing][b];
+                        sr[b].x = factor(sr[b].x);
+                    }
                 }
                 ok = ok && wait(s_full(slot), pair ? j : j >> 1);
                 if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
@@ -362,16 +365,6 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                 const int k0 = k_lo + j * KT;
                 const bool whole = k0 + KT - 1 <= p_low && (a.window == 0 || k0 > p_high - a.window);
                 const int last = pos - k0, first = a.window > 0 ? last - a.window : -1;  // seen: first < i <= last
-                // Half of the step's columns at a time (but see kParts): the MMAs of the first half's P
-                // run while the second half is computed.  Exponentials are taken against the reference
-                // that is there, with the half's maximum found beside them; where a row passes its
-                // reference by too much (the first step, seldom after it) the warp replaces it and
-                // computes the half again.  P takes the place of scores that were read, two values a
-                // column.
-                constexpr int kHalf = KT / P::kParts, kHalfBlocks = kHalf / 16, kChunks = kHalf / 32;
-                uint32_t s[P::kParts][kChunks][32];
-#pragma unroll
-                for (int c = 0; c < kChunks; ++c) ld32(s_at + 32 * c, s[0][c]);
                 auto rescale = [&](float f) {  // O times f
                     fence_after();
 #pragma unroll 1
@@ -384,91 +377,179 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                         st16(o_at + 16 * k, o);
                     }
                 };
+                if constexpr (STAGED) {
+                    // Half of the step's columns at a time (but see kParts): the MMAs of the first half's P
+                    // run while the second half is computed.  Exponentials are taken against the reference
+                    // that is there, with the half's maximum found beside them; where a row passes its
+                    // reference by too much (the first step, seldom after it) the warp replaces it and
+                    // computes the half again.  P takes the place of scores that were read, two values a
+                    // column.
+                    constexpr int kHalf = KT / kParts, kHalfBlocks = kHalf / 16, kChunks = kHalf / 32;
+                    uint32_t s[kParts][kChunks][32];
 #pragma unroll
-                for (int half = 0; half < P::kParts; ++half) {
-                    const float2 *v = sc + half * kHalfBlocks;
-                    uint32_t (&sh)[kChunks][32] = s[half];
-                    if (half == 1) {
+                    for (int c = 0; c < kChunks; ++c) ld32(s_at + 32 * c, s[0][c]);
 #pragma unroll
-                        for (int c = 0; c < kChunks; ++c) ld32(s_at + kHalf + 32 * c, sh[c]);
-                    }
+                    for (int half = 0; half < kParts; ++half) {
+                        const float2 *v = sr + half * kHalfBlocks;
+                        uint32_t (&sh)[kChunks][32] = s[half];
+                        if (half == 1) {
 #pragma unroll
-                    for (int c = 0; c < kChunks; ++c) ld_wait(sh[c]);
-                    if (!whole) {
-#pragma unroll
-                        for (int i = 0; i < kHalf; ++i)
-                            if (half * kHalf + i > last || half * kHalf + i <= first) sh[i / 32][i % 32] = 0xFF800000u;  // -inf
-                    }
-                    if constexpr (P::kParts == 1) {
-                        float mt = -INFINITY;
-#pragma unroll
-                        for (int b = 0; b < kHalfBlocks; ++b) {
-                            const uint32_t *x = &sh[b / 2][16 * (b & 1)];
-                            float top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-#pragma unroll
-                            for (int i = 2; i < 16; i += 2)
-                                top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
-                            mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
+                            for (int c = 0; c < kChunks; ++c) ld32(s_at + kHalf + 32 * c, sh[c]);
                         }
-                        if (__any_sync(0xffffffffu, mt > m + kGrow)) {
+#pragma unroll
+                        for (int c = 0; c < kChunks; ++c) ld_wait(sh[c]);
+                        if (!whole) {
+#pragma unroll
+                            for (int i = 0; i < kHalf; ++i)
+                                if (half * kHalf + i > last || half * kHalf + i <= first) sh[i / 32][i % 32] = 0xFF800000u;  // -inf
+                        }
+                        if constexpr (kParts == 1) {
+                            float mt = -INFINITY;
+#pragma unroll
+                            for (int b = 0; b < kHalfBlocks; ++b) {
+                                const uint32_t *x = &sh[b / 2][16 * (b & 1)];
+                                float top = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+#pragma unroll
+                                for (int i = 2; i < 16; i += 2)
+                                    top = fmaxf(fmaxf(top, __uint_as_float(x[i])), __uint_as_float(x[i + 1]));
+                                mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
+                            }
+                            if (__any_sync(0xffffffffu, mt > m + kGrow)) {
+                                const float mn = mt > m + kGrow ? mt : m;
+                                const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+                                m = mn;
+                                l *= f;
+                                if (j > 0) {
+                                    ok = __all_sync(0xffffffffu, wait(pv_done, j - 1));  // it still adds to O
+                                    if (!ok) break;
+                                    rescale(f);
+                                }
+                            }
+                        }
+                        float sum;
+                        while (true) {
+                            const float ms = m == -INFINITY ? 0.0f : m;
+                            float mt = -INFINITY;
+                            sum = 0.0f;
+#pragma unroll
+                            for (int b = 0; b < kHalfBlocks; ++b) {
+                                const uint32_t *x = &sh[b / 2][16 * (b & 1)];
+                                const float add = v[b].y - ms;
+                                const uint64_t ff = two(v[b].x, v[b].x), aa = two(add, add);
+                                uint64_t part = two(0.0f, 0.0f);
+                                float top = -INFINITY;
+                                uint32_t p[8];
+#pragma unroll
+                                for (int i = 0; i < 16; i += 2) {
+                                    const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
+                                    const float2 y = untwo(fma2(two(x0, x1), ff, aa));
+                                    const float e0 = ex2(y.x), e1 = ex2(y.y);
+                                    top = fmaxf(fmaxf(top, x0), x1);
+                                    part = add2(part, two(e0, e1));
+                                    p[i / 2] = Half2Of<__half>::pack(e0, e1);
+                                }
+                                if (kParts > 1) mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
+                                const float2 t = untwo(part);
+                                sum = fmaf(t.x + t.y, ex2(-v[b].y), sum);
+                                st8(s_at + half * (kHalf / 2) + 8 * b, p);
+                            }
+                            if (kParts == 1 || !__any_sync(0xffffffffu, mt > m + kGrow)) break;
                             const float mn = mt > m + kGrow ? mt : m;
                             const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
                             m = mn;
                             l *= f;
-                            if (j > 0) {
-                                ok = __all_sync(0xffffffffu, wait(pv_done, j - 1));  // it still adds to O
+                            if (j > 0 || half) {
+                                // what still adds to O: the first half's product, or with one tile
+                                // that of the step before (with two it is done before S comes)
+                                if (!pair && j > 0) ok = wait(pv_done, j - 1);
+                                if (ok && half) ok = wait(pv_half(w), j);
+                                ok = __all_sync(0xffffffffu, ok);
                                 if (!ok) break;
                                 rescale(f);
                             }
                         }
+                        if (!ok) break;
+                        l += sum;
+                        st_wait();
+                        fence_before();
+                        mbar_arrive(p_full(slot, half));
                     }
-                    float sum;
-                    while (true) {
-                        const float ms = m == -INFINITY ? 0.0f : m;
-                        float mt = -INFINITY;
-                        sum = 0.0f;
+                } else {
+                    // A small loop over 32 columns: unrolled over the step, this role and the converting
+                    // ones outgrow the instruction cache and 128 registers (2048 queries at 8192 keys,
+                    // head_dim 64 / 128 / 256: 337 / 473 / 713 us as a loop, 436 / 693 / 790 unrolled; 8 x 12
+                    // of 128 at 8000 keys: 81 and 102).  Each load is waited for at once: nothing is in flight into
+                    // registers over the loop's code.
+                    const float2 *sc = scales[j % kScaleRing];
+#pragma unroll 1
+                    for (int c = 0; c < KT / 32; ++c) {
+                        uint32_t s[32];
+                        ld32(s_at + 32 * c, s);
+                        ld_wait(s);
+                        if (!whole) {
 #pragma unroll
-                        for (int b = 0; b < kHalfBlocks; ++b) {
-                            const uint32_t *x = &sh[b / 2][16 * (b & 1)];
-                            const float add = v[b].y - ms;
-                            const uint64_t ff = two(v[b].x, v[b].x), aa = two(add, add);
+                            for (int i = 0; i < 32; ++i)
+                                if (32 * c + i > last || 32 * c + i <= first) s[i] = 0xFF800000u;  // -inf
+                        }
+                        const float2 va = sc[2 * c], vb = sc[2 * c + 1];
+                        const float fa = factor(va.x), fb = factor(vb.x);
+                        float ta = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
+                        float tb = fmaxf(__uint_as_float(s[16]), __uint_as_float(s[17]));
+#pragma unroll
+                        for (int i = 2; i < 16; i += 2) {
+                            ta = fmaxf(fmaxf(ta, __uint_as_float(s[i])), __uint_as_float(s[i + 1]));
+                            tb = fmaxf(fmaxf(tb, __uint_as_float(s[16 + i])), __uint_as_float(s[17 + i]));
+                        }
+                        const float mt = fmaxf(fmaf(ta, fa, va.y), fmaf(tb, fb, vb.y));
+                        if (__any_sync(0xffffffffu, mt > m + kGrow)) {
+                            // a new reference, a whole power of two away: l, this step's P so far and O follow
+                            const float mn = mt > m + kGrow ? (m == -INFINITY ? mt : m + ceilf(mt - m)) : m;
+                            const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
+                            m = mn;
+                            l *= f;
+                            st_wait();
+#pragma unroll 1
+                            for (int k = 0; k < c; ++k) {
+                                uint32_t p[16];
+                                ld16(s_at + 16 * k, p);
+                                ld_wait(p);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) {
+                                    const float2 v = Half2Of<__half>::f2(p[i]);  // f itself may be below fp16's range
+                                    p[i] = Half2Of<__half>::pack(v.x * f, v.y * f);
+                                }
+                                st16(s_at + 16 * k, p);
+                            }
+                            if (j > 0) {
+                                if (!pair) ok = __all_sync(0xffffffffu, wait(pv_done, j - 1));  // it still adds to O
+                                if (!ok) break;
+                                rescale(f);
+                            }
+                        }
+                        const float ms = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t p[8];  // takes the place of S in TMEM, two values a column
+                            const float f = h ? fb : fa, lv = h ? vb.y : va.y, add = lv - ms;
+                            const uint64_t ff = two(f, f), aa = two(add, add);
                             uint64_t part = two(0.0f, 0.0f);
-                            float top = -INFINITY;
-                            uint32_t p[8];
 #pragma unroll
                             for (int i = 0; i < 16; i += 2) {
-                                const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
-                                const float2 y = untwo(fma2(two(x0, x1), ff, aa));
-                                const float e0 = ex2(y.x), e1 = ex2(y.y);
-                                top = fmaxf(fmaxf(top, x0), x1);
+                                const float2 x = untwo(fma2(two(__uint_as_float(s[16 * h + i]),
+                                                                __uint_as_float(s[16 * h + i + 1])), ff, aa));
+                                const float e0 = ex2(x.x), e1 = ex2(x.y);
                                 part = add2(part, two(e0, e1));
                                 p[i / 2] = Half2Of<__half>::pack(e0, e1);
                             }
-                            if (P::kParts > 1) mt = fmaxf(mt, fmaf(top, v[b].x, v[b].y));
                             const float2 t = untwo(part);
-                            sum = fmaf(t.x + t.y, ex2(-v[b].y), sum);
-                            st8(s_at + half * (kHalf / 2) + 8 * b, p);
-                        }
-                        if (P::kParts == 1 || !__any_sync(0xffffffffu, mt > m + kGrow)) break;
-                        const float mn = mt > m + kGrow ? mt : m;
-                        const float f = mn == -INFINITY ? 1.0f : ex2(m - mn);
-                        m = mn;
-                        l *= f;
-                        if (j > 0 || half) {
-                            // what still adds to O: the first half's product, or with one tile
-                            // that of the step before (with two it is done before S comes)
-                            if (!pair && j > 0) ok = wait(pv_done, j - 1);
-                            if (ok && half) ok = wait(pv_half(w), j);
-                            ok = __all_sync(0xffffffffu, ok);
-                            if (!ok) break;
-                            rescale(f);
+                            l = fmaf(t.x + t.y, ex2(-lv), l);
+                            st8(s_at + 16 * c + 8 * h, p);
                         }
                     }
                     if (!ok) break;
-                    l += sum;
                     st_wait();
                     fence_before();
-                    mbar_arrive(p_full(slot, half));
+                    mbar_arrive(p_full(slot, 0));
                 }
                 if (!ok) break;
             }
@@ -678,12 +759,12 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
         auto pv = [&](int j, int w, int slot, int half) {
             const uint32_t v = v_lo + (j % kStages) * (P::kKV / 16);
 #pragma unroll
-            for (int i = 0; i < KT / (16 * P::kParts); ++i) {
-                const int s = half * (KT / (16 * P::kParts)) + i;
+            for (int i = 0; i < KT / (16 * kParts); ++i) {
+                const int s = half * (KT / (16 * kParts)) + i;
                 mma_ts(tmem + (w ? P::kO1 : P::kO0), tmem + (slot ? P::kS1 : 0) + 8 * s, v + s * (16 * 128 / 16), hi_word,
                        i_pv, j > 0 || s > 0);
             }
-            if (half + 1 < P::kParts) commit(pv_half(w));
+            if (half + 1 < kParts) commit(pv_half(w));
         };
         // What ordinary stores wrote (Q, and the tiles of the direct form) is read by the MMAs: the
         // fence between the two stands here, after the wait, because the writers have loads in
@@ -694,7 +775,7 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
         };
         auto all = [&](uint32_t b, uint32_t parity) { return __all_sync(0xffffffffu, wait(b, parity)) != 0; };
         auto both = [&](int j, int w, int slot, int parity) {  // O += P V of a step, by parts
-            for (int half = 0; half < P::kParts; ++half) {
+            for (int half = 0; half < kParts; ++half) {
                 if (!all(p_full(slot, half), parity)) return false;
                 fence_after();
                 pv(j, w, slot, half);
@@ -914,7 +995,8 @@ int splits_of(const AttendArgs &a)
 }
 
 // One query tile reads each code once: it converts them itself.  (Staging costs
-// five bytes of traffic a code: 8 sequences of 8000 tokens, 11 queries: 137 us.)
+// five bytes of traffic a code: 8 sequences of 8000 tokens, 11 queries: 137 us
+// staged, 81 not; 2 x 256 queries of 8192 tokens, six tiles a head: 136 and 145.)
 template <int D>
 bool stages(const AttendArgs &a)
 {
