@@ -338,16 +338,21 @@ class KVCache:
                 return self.truncate(keep, out=out)
         return self.fork(torch.arange(self.rows, dtype=torch.int32, device=self.device), keep, out=out)
 
-    def compact(self, *, out=None, stream=None):
+    def compact(self, *, out=None, work=None, stream=None):
         """Moves the live pages to the low end of the pool (bqd_kv_compact).  Returns the cache
-        that takes this one's place and an int32 [1] count of the pages that moved."""
+        that takes this one's place and an int32 [1] count of the pages that moved.  ``work``
+        (int32 [2 * pages], else allocated) holds page q's new index in work[pages + q]
+        afterwards: a caller that pins pages (counts of its own in refs) follows them by it."""
+        if work is not None:
+            _dense(work, "work", torch.int32, (2 * self.pages,), self.device)
         on = self._on(stream)
         if on is not None:
             with on:
-                return self.compact(out=out)
+                return self.compact(out=out, work=work)
         new = self._sibling(self.rows, out)
-        work = torch.empty(2 * self.pages + 1, dtype=torch.int32, device=self.device)
-        moved = work[2 * self.pages:]
+        moved = torch.empty(1, dtype=torch.int32, device=self.device)
+        if work is None:
+            work = torch.empty(2 * self.pages, dtype=torch.int32, device=self.device)
         _check("bqd_kv_compact", self._lib.bqd_kv_compact(self._ref, new._ref, work.data_ptr(), moved.data_ptr(),
                                                           self._stream()))
         return new, moved

@@ -353,7 +353,10 @@ int bqd_kv_fork(const bqd_kv_cache *from, const bqd_kv_cache *to, const int32_t 
  * L moves to the k-th free index below L, in every layer; `to` gets the table,
  * lens and refs that follow (other memory than those of `from`; pools and
  * sizes are the same).  The bytes of a page that moved away stay as they are.
- *   work    device int32 [2 * pages], scratch
+ * Pages that only a pin of the caller holds move too.
+ *   work    device int32 [2 * pages]: scratch in the first half; work[pages + q]
+ *           is the new index of page q (q where it stayed), for what the caller
+ *           knows by its index
  *   moved   device int32 [1]: pages moved
  */
 int bqd_kv_compact(const bqd_kv_cache *from, const bqd_kv_cache *to, int32_t *work, int32_t *moved,
