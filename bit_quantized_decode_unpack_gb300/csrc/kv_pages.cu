@@ -10,7 +10,7 @@
 // by memory (16-byte accesses, 64 bytes a thread in flight): 525 MB of moves with
 // their plan 97 us (5431 GB/s, 81% of a measured copy; about 8 us are the plan).
 // 64 beams of 16 parents with their copies: 19 us on the GPU in three launches,
-// 32 us a call of fork and reserve from Python.
+// 32 to 47 us a call of fork and reserve from Python, by the host.
 #include <algorithm>
 
 #include "kv_common.cuh"

@@ -274,6 +274,8 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
             const uint32_t q_tile = base + w * (P::kPanels * P::kPanelQ);
             const int row0 = (warp & 3) * 32;  // the warp's rows of the tile
             // ---- q: scaled by 2^-e into fp16 (e of the row's largest magnitude) ----
+            // fp16 keeps every bit of a bf16 value down to 2^-16 of that magnitude, and an absolute
+            // 2^-25 of it below, of the order of what the fp32 sum of the scores rounds off
             // D / 8 lanes take a row, 16 bytes each, up to 16 passes in flight (one row a thread
             // took 8 us: each load touched 32 rows)
             constexpr int kRowLanes = D / 8, kRowsPass = 32 / kRowLanes, kPasses = kRowLanes;
@@ -976,7 +978,7 @@ int64_t most_steps(const AttendArgs &a)
 // of a full tile, over the waves of CTAs (one an SM).  A CTA costs about three
 // steps to begin and end, and to leave and join its O three and a half more
 // (2 x 128 KB at an SM's share of the bandwidth): 64 queries at 8192 keys, 48
-// heads: 129 us with one, 31 us with nine.
+// heads: 125 us with one, 45 us with nine.
 template <int D>
 int splits_of(const AttendArgs &a)
 {

@@ -249,8 +249,11 @@ class KVCache:
         q: fp16 or bf16 [tokens, q_heads, head_dim], any strides of token and head; the cache
         already holds the queries' own tokens.  ``window`` > 0 keeps the last ``window`` keys
         of each query; ``scale`` defaults to 1 / sqrt(head_dim); ``max_len`` bounds the rows'
-        lengths where the caller knows them (only speed depends on it).  Returns
-        (out [tokens, q_heads, head_dim], lse fp32 [tokens, q_heads])."""
+        lengths where the caller knows them (only speed depends on it).  With ``starts``, give
+        ``max_new``, the most queries of a row: it selects the kernel and sizes the scratch, and
+        without it a batch of single tokens is planned as one row of them all.  Returns
+        (out [tokens, q_heads, head_dim], lse fp32 [tokens, q_heads]); tokens that no row has,
+        and a row's queries beyond ``max_new``, are not written."""
         kind = self._half(q, "q", None)
         tokens, heads, d = q.shape
         if heads == 0 or heads % self.kv_heads:

@@ -267,7 +267,7 @@ typedef struct bqd_kv_cache {
  *   base    device int32 [rows];  starts device int32 [rows + 1] or NULL
  *   tokens  rows of k and v (== rows when starts is NULL)
  *   max_new an upper bound of starts[r+1] - starts[r] (later tokens of a row
- *           are not stored)
+ *           are not stored), cut to `tokens`
  * A page that two rows list must not be appended to through either
  * (bqd_kv_reserve replaces it).  Returns BQD_OK, BQD_ERR_INVALID_ARG,
  * BQD_ERR_ALIGNMENT or BQD_ERR_CUDA.
@@ -288,7 +288,12 @@ int bqd_kv_append(const bqd_kv_cache *cache, int layer, const void *k, int64_t k
  * A query that sees no key (an empty row, or p < 0) gives 0 and -infinity.
  * Scores, softmax sums and outputs accumulate in fp32; the weights that meet
  * V are rounded to fp16 after a power-of-two scaling that keeps the largest
- * near 1.
+ * near 1.  bf16 queries are taken in fp16, scaled by a power of two: elements
+ * below 2^-16 of a query's largest lose bits, 2^-25 of that largest at most.
+ * A weight times its block's V scale that is below 2^-126 of the row's largest
+ * such product counts as 0, in out and lse: blocks of zeros (their V scale is
+ * near 2^-87) stay in the sum beside values of V up to 4e6 where their weight is
+ * above 2^-24 of the largest.
  *   q       device [tokens, q_heads, head_dim] of `dtype` (F16 or BF16), strides
  *           of token and head in elements, head_dim contiguous
  *   out     device [tokens, q_heads, head_dim] of `dtype`, dense, 16-byte
@@ -296,7 +301,9 @@ int bqd_kv_append(const bqd_kv_cache *cache, int layer, const void *k, int64_t k
  *   lse     device fp32 [tokens, q_heads] or NULL
  *   max_new an upper bound of starts[r+1] - starts[r].  A row's later queries,
  *           and those past `tokens`, are not computed; the others keep the
- *           positions that the row's true count n gives them
+ *           positions that the row's true count n gives them.  It also decides
+ *           between the kernels for few and for many queries and plans the
+ *           scratch, so a loose bound costs time
  *   max_len a bound of lens that the launch is planned for (0: the table's
  *           capacity); longer rows stay correct
  *   scale   finite;  window >= 0 (0: none)
