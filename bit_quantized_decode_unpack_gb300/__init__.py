@@ -82,7 +82,8 @@ def load() -> ctypes.CDLL:
         lib.bqd_set_option.restype = i32
         lib.bqd_get_option.argtypes = [i32]
         lib.bqd_get_option.restype = i64
-        kv_cache.declare(lib)
+        for part in (kv_cache, rope, drafts, logprobs):
+            part.declare(lib)
         if lib.bqd_abi_version() != ABI_VERSION:
             raise RuntimeError(f"libbqd ABI {lib.bqd_abi_version()} != binding ABI {ABI_VERSION}")
         _lib = lib
@@ -341,6 +342,9 @@ def device_status(stream=None) -> int:
     return int(load().bqd_device_status(_stream(stream)))
 
 
-from . import kv_cache  # noqa: E402
+from . import drafts, kv_cache, logprobs, rope  # noqa: E402
 from .kv_cache import (KVCache, kv_append, kv_attend, kv_attend_workspace, kv_compact,  # noqa: E402,F401
-                       kv_copy_pages, kv_fork, kv_reserve)
+                       kv_accept, kv_attend_masked, kv_copy_pages, kv_fork, kv_reserve)
+from .drafts import spec_tree_verify, tree_mask  # noqa: E402,F401
+from .logprobs import TokenLogprobs, token_logprobs  # noqa: E402,F401
+from .rope import QKNormRope, qk_norm_rope, rope_frequencies  # noqa: E402,F401

@@ -148,13 +148,16 @@ extern "C" int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_head
     a.max_new = (int)max_new;
     a.max_len = planned_length(c, max_len);
     a.window = (int)(window < most ? window : 0);
+    a.mask = nullptr, a.depth = nullptr, a.words = 0;
     return scratch_need(a);
 }
 
-extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride,
-                             int64_t q_head_stride, int dtype, int q_heads, const int32_t *starts, int64_t tokens,
-                             int64_t max_new, int64_t max_len, float scale, int64_t window, void *out, float *lse,
-                             void *work, int64_t work_bytes, bqd_stream_t stream)
+namespace {
+
+int attend_common(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride, int64_t q_head_stride,
+                  int dtype, int q_heads, const int32_t *starts, int64_t tokens, int64_t max_new, int64_t max_len,
+                  float scale, int64_t window, const uint64_t *mask, int words, const int32_t *depth, void *out,
+                  float *lse, void *work, int64_t work_bytes, bqd_stream_t stream)
 {
     const int st = check_cache(cache);
     if (st != BQD_OK) return st;
@@ -171,7 +174,8 @@ extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q
     if (max_new > tokens) max_new = tokens;
     if (max_new * group >= most) return BQD_ERR_INVALID_ARG;
     if (!q || !out) return BQD_ERR_INVALID_ARG;
-    if (!at(q, 2) || !at(out, 16) || !at(lse, 4) || !at(starts, 4) || !at(work, 16)) return BQD_ERR_ALIGNMENT;
+    if (!at(q, 2) || !at(out, 16) || !at(lse, 4) || !at(starts, 4) || !at(work, 16) || !at(mask, 8) || !at(depth, 4))
+        return BQD_ERR_ALIGNMENT;
     AttendArgs a;
     a.L = layer_of(c, layer);
     a.q = q, a.q_token = q_token_stride, a.q_head = q_head_stride;
@@ -184,10 +188,34 @@ extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q
     a.max_len = planned_length(c, max_len);
     a.window = (int)(window < most ? window : 0);  // one past any position hides nothing
     a.q_vec = vec_ok(q, q_token_stride, q_head_stride);
+    a.mask = mask, a.words = words, a.depth = depth;
     a.work = nullptr;
     const int64_t need = scratch_need(a);
     if (need > 0 && work_bytes >= need) a.work = work;
     return many_queries(a) ? launch_attend_prefill(a, to_stream(stream)) : launch_attend_decode(a, to_stream(stream));
+}
+
+}  // namespace
+
+extern "C" int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride,
+                             int64_t q_head_stride, int dtype, int q_heads, const int32_t *starts, int64_t tokens,
+                             int64_t max_new, int64_t max_len, float scale, int64_t window, void *out, float *lse,
+                             void *work, int64_t work_bytes, bqd_stream_t stream)
+{
+    return attend_common(cache, layer, q, q_token_stride, q_head_stride, dtype, q_heads, starts, tokens, max_new, max_len,
+                         scale, window, nullptr, 0, nullptr, out, lse, work, work_bytes, stream);
+}
+
+extern "C" int bqd_kv_attend_masked(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride,
+                                    int64_t q_head_stride, int dtype, int q_heads, const int32_t *starts, int64_t tokens,
+                                    int64_t max_new, int64_t max_len, float scale, int64_t window, const uint64_t *mask,
+                                    int words, const int32_t *depth, void *out, float *lse, void *work,
+                                    int64_t work_bytes, bqd_stream_t stream)
+{
+    if (words < 1 || words > BQD_TREE_MAX_WORDS || (window > 0 && !depth)) return BQD_ERR_INVALID_ARG;
+    if (!mask && tokens > 0) return BQD_ERR_INVALID_ARG;
+    return attend_common(cache, layer, q, q_token_stride, q_head_stride, dtype, q_heads, starts, tokens, max_new, max_len,
+                         scale, window, mask, words, depth, out, lse, work, work_bytes, stream);
 }
 
 extern "C" int bqd_kv_reserve(const bqd_kv_cache *cache, const int32_t *counts, int32_t *base, int32_t *copies,
@@ -211,6 +239,18 @@ extern "C" int bqd_kv_fork(const bqd_kv_cache *from, const bqd_kv_cache *to, con
     if (!same_pools(*from, *to) || (to->rows > 0 && !parents)) return BQD_ERR_INVALID_ARG;
     if (!at(parents, 4) || !at(keep, 4)) return BQD_ERR_ALIGNMENT;
     return launch_fork(*from, *to, parents, keep, to_stream(stream));
+}
+
+extern "C" int bqd_kv_accept(const bqd_kv_cache *from, const bqd_kv_cache *to, const int32_t *path, int width,
+                             const int32_t *starts, bqd_stream_t stream)
+{
+    int st = check_cache(from);
+    if (st == BQD_OK) st = check_cache(to);
+    if (st != BQD_OK) return st;
+    if (!same_pools(*from, *to) || from->rows != to->rows || width < 1) return BQD_ERR_INVALID_ARG;
+    if (from->rows > 0 && !path) return BQD_ERR_INVALID_ARG;
+    if (!at(path, 4) || !at(starts, 4)) return BQD_ERR_ALIGNMENT;
+    return launch_accept(*from, *to, layer_of(*from, 0), path, width, starts, to_stream(stream));
 }
 
 extern "C" int bqd_kv_compact(const bqd_kv_cache *from, const bqd_kv_cache *to, int32_t *work, int32_t *moved,

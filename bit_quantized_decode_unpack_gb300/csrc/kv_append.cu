@@ -35,30 +35,6 @@ struct AppendParams {
     int tokens, max_new, blocks; // blocks: of a row that max_new tokens can touch
 };
 
-template <int FMT>
-__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
-{
-    if constexpr (FMT == BQD_KV_INT8) {
-        // 1.5 * 2^23 + t has the integer nearest to t (ties to even) in its low bits
-        const float m = 12582912.0f;
-        const uint32_t ua = __float_as_uint(__fadd_rn(a, m)), ub = __float_as_uint(__fadd_rn(b, m));
-        const uint32_t uc = __float_as_uint(__fadd_rn(c, m)), ud = __float_as_uint(__fadd_rn(d, m));
-        return __byte_perm(__byte_perm(ua, ub, 0x0040), __byte_perm(uc, ud, 0x0040), 0x5410);
-    } else {
-        uint16_t lo, hi;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
-        return (uint32_t)lo | ((uint32_t)hi << 16);
-    }
-}
-
-// x r of a value that may be infinite or NaN
-template <int FMT>
-__device__ __forceinline__ float tame(float t)
-{
-    return t != t ? 0.0f : fminf(fmaxf(t, -Code<FMT>::kTop), Code<FMT>::kTop);
-}
-
 template <typename T, bool VEC>
 __device__ __forceinline__ uint4 load8(const T *p)
 {

@@ -143,7 +143,9 @@ struct Shares {
     int count;      // 0: clusters
 };
 
-// What the queries of a column tile see
+// What the queries of a column tile see.  Masked: each sees the tokens before its row's
+// last `rest` ones, and of those what its mask says.
+template <bool MASKED>
 struct View {
     Span span;
     int L, cols, c0, p_min, p_max, lo, hi;
@@ -154,10 +156,17 @@ struct View {
         cols = span.n * a.group;  // columns: query-major, then head of the group
         c0 = ctile * kCols;
         const int i_min = c0 / a.group, i_max = (min(c0 + kCols, cols) - 1) / a.group;
-        p_min = L - span.rest + i_min;
-        p_max = L - span.rest + i_max;
-        hi = max(0, p_max + 1);
-        lo = a.window > 0 ? max(0, p_min + 1 - a.window) : 0;
+        if constexpr (MASKED) {
+            p_min = L - span.rest - 1;  // what every query sees but for a window
+            p_max = L - 1;              // no position is later
+            hi = L;
+            lo = a.window > 0 ? max(0, p_min + 2 - a.window) : 0;
+        } else {
+            p_min = L - span.rest + i_min;
+            p_max = L - span.rest + i_max;
+            hi = max(0, p_max + 1);
+            lo = a.window > 0 ? max(0, p_min + 1 - a.window) : 0;
+        }
     }
 };
 
@@ -192,8 +201,8 @@ __device__ __forceinline__ void finish(const AttendArgs &a, int lo, int cols, in
 
 // Columns of a unit against its tiles [j0, j1): each warp takes every kWarps-th.
 // The joined (o, m, l) of each quad of dims goes to emit(col, d, o, m, l).
-template <typename T, int D, int FMT, int NT, typename Emit>
-__device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_, int row, int head, int j0, int j1,
+template <typename T, int D, int FMT, int NT, bool MASKED, typename Emit>
+__device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View<MASKED> &vw_, int row, int head, int j0, int j1,
                                            float *smem, Emit emit)
 {
     using C = Code<FMT>;
@@ -253,7 +262,7 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_,
     // q: column n*8 + g, the dims of this lane's K chunks, scaled by 2^-e
     uint32_t qf[NT][KS][2];
     float cs[NT][2];             // f 2^e of columns n*8 + 2t, + 2t + 1
-    int pos[NT][2];              // their positions (-1: nothing)
+    int pos[NT][2];              // their positions (masked: their tokens); -1: nothing
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int c = c0 + n * 8 + g;
@@ -303,7 +312,7 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_,
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int cc = c0 + n * 8 + 2 * t + h;
-            pos[n][h] = cc < cols ? L - span.rest + cc / a.group : -1;
+            pos[n][h] = cc < cols ? (MASKED ? span.lo : L - span.rest) + cc / a.group : -1;
         }
     }
 
@@ -353,7 +362,18 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_,
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int tok = t0 + g + 8 * (e >> 1), pp = pos[n][e & 1];
-                    if (tok > pp || (a.window > 0 && tok <= pp - a.window)) s[n][e] = -INFINITY;
+                    if constexpr (MASKED) {
+                        const int node = tok - (L - span.rest);  // < 0: before the row's last tokens
+                        bool sees = pp >= 0 && tok < L;
+                        if (sees && node >= 0)
+                            sees = node < 64 * a.words &&
+                                   (__ldg(a.mask + (int64_t)pp * a.words + (node >> 6)) >> (node & 63) & 1) != 0;
+                        else if (sees && a.window > 0)
+                            sees = node > max(0, min(__ldg(a.depth + pp), span.rest - 1)) - a.window;
+                        if (!sees) s[n][e] = -INFINITY;
+                    } else {
+                        if (tok > pp || (a.window > 0 && tok <= pp - a.window)) s[n][e] = -INFINITY;
+                    }
                 }
             }
             grow |= fmaxf(s[n][0], s[n][2]) > m[n][0] + kGrow || fmaxf(s[n][1], s[n][3]) > m[n][1] + kGrow;
@@ -464,7 +484,7 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const View &vw_,
     __syncthreads();  // the partials' place may be written again
 }
 
-template <typename T, int D, int FMT, int NT>
+template <typename T, int D, int FMT, int NT, bool MASKED>
 __global__ void __launch_bounds__(Tile<D, NT>::kThreads, Tile<D, NT>::kResident)
 attend_cluster_kernel(const AttendArgs a, int S)
 {
@@ -472,14 +492,14 @@ attend_cluster_kernel(const AttendArgs a, int S)
     extern __shared__ __align__(16) float smem[];
     const int rank = S > 1 ? (int)cluster_ctarank() : 0;
     const int ctile = blockIdx.x / S, head = blockIdx.y, row = blockIdx.z;
-    const View v(a, row, ctile, TL::kCols);
+    const View<MASKED> v(a, row, ctile, TL::kCols);
     if (v.c0 >= v.cols) return;              // the whole cluster leaves
     // this CTA's tiles of 16 tokens
     const int tile_lo = v.lo >> 4, tiles = max(0, ((v.hi + 15) >> 4) - tile_lo);
     const int j0 = tile_lo + (int)((int64_t)tiles * rank / S), j1 = tile_lo + (int)((int64_t)tiles * (rank + 1) / S);
     float *joined = smem + TL::kWarps * (TL::kWarpFloats + 2 * TL::kCols);  // [col][kPitch]
     float *jm = joined + TL::kWarpFloats, *jl = jm + TL::kCols;
-    unit_tiles<T, D, FMT, NT>(a, v, row, head, j0, j1, smem, [&](int col, int d, float4 o, float mm, float ll) {
+    unit_tiles<T, D, FMT, NT, MASKED>(a, v, row, head, j0, j1, smem, [&](int col, int d, float4 o, float mm, float ll) {
         if (S == 1) {
             finish<T, D>(a, v.span.lo, v.cols, v.c0, head, col, d, o, mm, ll);
         } else {
@@ -508,7 +528,7 @@ attend_cluster_kernel(const AttendArgs a, int S)
     cluster_sync();  // no CTA leaves while another reads its shared memory
 }
 
-template <typename T, int D, int FMT, int NT>
+template <typename T, int D, int FMT, int NT, bool MASKED>
 __global__ void __launch_bounds__(Tile<D, NT>::kThreads, Tile<D, NT>::kResident)
 attend_shares_kernel(const AttendArgs a, const Shares sh)
 {
@@ -572,13 +592,13 @@ attend_shares_kernel(const AttendArgs a, const Shares sh)
         const int unit = (int)(off / cost), j = (int)(off - (int64_t)unit * cost);
         const int head = unit % a.L.heads, ctile = unit / a.L.heads;
         const int stop = (int)min((int64_t)cost, j + (end - pos));
-        const View v(a, row, ctile, TL::kCols);
+        const View<MASKED> v(a, row, ctile, TL::kCols);
         const bool starts = j == 0, ends = stop == cost;
         float *piece = sh.pieces + ((int64_t)share * 2 + (starts ? 1 : 0)) * TL::kPiece;
         // tiles that this column tile sees of them
         const int j0 = max(rt.lo + max(0, j - kUnitCost), v.lo >> 4);
         const int j1 = min(rt.lo + max(0, stop - kUnitCost), (v.hi + 15) >> 4);
-        unit_tiles<T, D, FMT, NT>(a, v, row, head, j0, j1, smem, [&](int col, int d, float4 o, float mm, float ll) {
+        unit_tiles<T, D, FMT, NT, MASKED>(a, v, row, head, j0, j1, smem, [&](int col, int d, float4 o, float mm, float ll) {
             if (starts && ends) {
                 finish<T, D>(a, v.span.lo, v.cols, v.c0, head, col, d, o, mm, ll);
             } else {
@@ -691,9 +711,9 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
     cfg.attrs = attr;
     const int shares = a.work ? shares_of<D, NT>(a) : 0;
     if (shares > 0) {
-        auto kern = attend_shares_kernel<T, D, FMT, NT>;
-        static bool done[64] = {};
-        if (!configure(kern, TL::kSmem, done)) return BQD_ERR_CUDA;
+        auto kern = a.mask ? attend_shares_kernel<T, D, FMT, NT, true> : attend_shares_kernel<T, D, FMT, NT, false>;
+        static bool done[2][64] = {};
+        if (!configure(kern, TL::kSmem, done[a.mask != nullptr])) return BQD_ERR_CUDA;
         Shares sh;
         sh.pieces = static_cast<float *>(a.work);
         sh.cuts = reinterpret_cast<Cut *>(sh.pieces + (int64_t)shares * 2 * TL::kPiece);
@@ -708,9 +728,9 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
         cfg.numAttrs = 1;
         return cuda_status(cudaLaunchKernelEx(&cfg, attend_join_kernel<T, D, NT>, a, sh));
     }
-    auto kern = attend_cluster_kernel<T, D, FMT, NT>;
-    static bool done[64] = {};
-    if (!configure(kern, TL::kSmem, done)) return BQD_ERR_CUDA;
+    auto kern = a.mask ? attend_cluster_kernel<T, D, FMT, NT, true> : attend_cluster_kernel<T, D, FMT, NT, false>;
+    static bool done[2][64] = {};
+    if (!configure(kern, TL::kSmem, done[a.mask != nullptr])) return BQD_ERR_CUDA;
     const int64_t ctiles = ((int64_t)a.max_new * a.group + TL::kCols - 1) / TL::kCols;
     const int64_t units = ctiles * a.L.heads * a.L.rows;
     // split the keys until there are two CTAs an SM, as long as each warp

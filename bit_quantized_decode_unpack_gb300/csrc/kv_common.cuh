@@ -141,6 +141,33 @@ struct Code<BQD_KV_E4M3> {
     }
 };
 
+// ---- codes from fp32 -----------------------------------------------------------
+// Round to nearest even; int8 takes values within +-127.
+
+template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d)
+{
+    if constexpr (FMT == BQD_KV_INT8) {
+        // 1.5 * 2^23 + t has the integer nearest to t (ties to even) in its low bits
+        const float m = 12582912.0f;
+        const uint32_t ua = __float_as_uint(__fadd_rn(a, m)), ub = __float_as_uint(__fadd_rn(b, m));
+        const uint32_t uc = __float_as_uint(__fadd_rn(c, m)), ud = __float_as_uint(__fadd_rn(d, m));
+        return __byte_perm(__byte_perm(ua, ub, 0x0040), __byte_perm(uc, ud, 0x0040), 0x5410);
+    } else {
+        uint16_t lo, hi;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(b), "f"(a));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(d), "f"(c));
+        return (uint32_t)lo | ((uint32_t)hi << 16);
+    }
+}
+
+// x r of a value that may be infinite or NaN
+template <int FMT>
+__device__ __forceinline__ float tame(float t)
+{
+    return t != t ? 0.0f : fminf(fmaxf(t, -Code<FMT>::kTop), Code<FMT>::kTop);
+}
+
 // Request of bqd_kv_attend after host validation.
 struct AttendArgs {
     Layer L;
@@ -153,6 +180,11 @@ struct AttendArgs {
     int dtype, format, head_dim, q_heads, group;
     int tokens, max_new, max_len, window;
     bool q_vec;               // 16-byte loads of q are possible
+    // masked calls: which of its row's last tokens a query sees (its mask's bits), and its position
+    // from the first of them (only where there is a window); nullptr: causal
+    const uint64_t *mask;     // [tokens, words]
+    const int32_t *depth;     // [tokens]
+    int words;
     void *work;               // scratch of decode_workspace / prefill_workspace bytes, or nullptr
 };
 
@@ -173,8 +205,11 @@ int64_t decode_workspace(const AttendArgs &a);   // bytes of their scratch
 int64_t prefill_workspace(const AttendArgs &a);
 int launch_reserve(const bqd_kv_cache &c, const int32_t *counts, int32_t *base, int32_t *copies, int32_t *status,
                    cudaStream_t s);
+// parents == nullptr: each row its own
 int launch_fork(const bqd_kv_cache &from, const bqd_kv_cache &to, const int32_t *parents, const int32_t *keep,
                 cudaStream_t s);
+int launch_accept(const bqd_kv_cache &from, const bqd_kv_cache &to, const Layer &first, const int32_t *path, int width,
+                  const int32_t *starts, cudaStream_t s);
 int launch_compact(const bqd_kv_cache &from, const bqd_kv_cache &to, int32_t *work, int32_t *moved, cudaStream_t s);
 int launch_copy_pages(const bqd_kv_cache &c, const int32_t *src, const int32_t *dst, int64_t n, cudaStream_t s);
 

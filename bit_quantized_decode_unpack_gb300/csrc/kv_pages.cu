@@ -271,7 +271,7 @@ __device__ __forceinline__ void fork_entry(const ForkParams &p, int64_t e)
     } else {
         const int64_t f = e - old_n;
         const int i = (int)(f / p.row_pages), j = (int)(f % p.row_pages);
-        const int par = p.parents[i];
+        const int par = p.parents ? p.parents[i] : i;
         int len = 0;
         if ((unsigned)par < (unsigned)p.rows) {
             len = max(0, min(p.lens[par], cap));

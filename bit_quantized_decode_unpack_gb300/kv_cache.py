@@ -36,6 +36,7 @@ _device = _raw_stream = None  # the current device's index, a device's current s
 _KINDS = {}      # element types of q, k and v
 PAGE_TOKENS = (16, 32, 64, 128, 256)
 HEAD_DIMS = (64, 128, 256)
+MASK_WORDS = 16  # BQD_TREE_MAX_WORDS
 
 
 class CacheStruct(ctypes.Structure):
@@ -54,12 +55,15 @@ def declare(lib):
     lib.bqd_kv_append.argtypes = [cp, i32, vp, i64, i64, vp, i64, i64, i32, vp, vp, i64, i64, vp]
     lib.bqd_kv_attend.argtypes = [cp, i32, vp, i64, i64, i32, i32, vp, i64, i64, i64, ctypes.c_float, i64, vp, vp, vp,
                                   i64, vp]
+    lib.bqd_kv_attend_masked.argtypes = [cp, i32, vp, i64, i64, i32, i32, vp, i64, i64, i64, ctypes.c_float, i64, vp, i32,
+                                         vp, vp, vp, vp, i64, vp]
+    lib.bqd_kv_accept.argtypes = [cp, cp, vp, i32, vp, vp]
     lib.bqd_kv_attend_workspace.argtypes = [cp, i32, i64, i64, i64, i64]
     lib.bqd_kv_reserve.argtypes = [cp, vp, vp, vp, vp, vp]
     lib.bqd_kv_fork.argtypes = [cp, cp, vp, vp, vp]
     lib.bqd_kv_compact.argtypes = [cp, cp, vp, vp, vp]
     lib.bqd_kv_copy_pages.argtypes = [cp, vp, vp, i64, vp]
-    for f in ("append", "attend", "reserve", "fork", "compact", "copy_pages"):
+    for f in ("append", "attend", "attend_masked", "reserve", "fork", "accept", "compact", "copy_pages"):
         getattr(lib, f"bqd_kv_{f}").restype = i32
     lib.bqd_kv_attend_workspace.restype = i64
 
@@ -243,7 +247,7 @@ class KVCache:
             base.data_ptr(), at, tokens, max_new, self._stream()))
 
     def attend(self, q, starts=None, *, layer: int = 0, scale=None, window: int = 0, max_new=None, max_len: int = 0,
-               out=None, lse=None, stream=None):
+               mask=None, depth=None, out=None, lse=None, stream=None):
         """Causal attention of the rows' last tokens over the cache (bqd_kv_attend).
 
         q: fp16 or bf16 [tokens, q_heads, head_dim], any strides of token and head; the cache
@@ -251,7 +255,13 @@ class KVCache:
         of each query; ``scale`` defaults to 1 / sqrt(head_dim); ``max_len`` bounds the rows'
         lengths where the caller knows them (only speed depends on it).  With ``starts``, give
         ``max_new``, the most queries of a row: it selects the kernel and sizes the scratch, and
-        without it a batch of single tokens is planned as one row of them all.  Returns
+        without it a batch of single tokens is planned as one row of them all.
+
+        ``mask`` (int64 [tokens, words], of ``tree_mask`` or any other) replaces the causal rule
+        among a row's last n tokens, the n that starts gives it: every query sees the tokens before
+        them, and of the n those whose bit is set in its words (bqd_kv_attend_masked).  With a
+        window, ``depth`` (int32 [tokens]) places a query at the length before the n plus its
+        depth, and the window hides tokens before the n; the mask alone decides on the n.  Returns
         (out [tokens, q_heads, head_dim], lse fp32 [tokens, q_heads]); tokens that no row has,
         and a row's queries beyond ``max_new``, are not written."""
         kind = self._half(q, "q", None)
@@ -261,11 +271,13 @@ class KVCache:
         at, max_new = self._ragged(starts, tokens, max_new)
         if window < 0 or max_len < 0:
             raise ValueError("window and max_len must be >= 0")
+        if mask is not None or depth is not None:
+            self._masks(mask, depth, tokens, window)
         on = self._on(stream)
         if on is not None:
             with on:
                 return self.attend(q, starts, layer=layer, scale=scale, window=window, max_new=max_new,
-                                   max_len=max_len, out=out, lse=lse)
+                                   max_len=max_len, mask=mask, depth=depth, out=out, lse=lse)
         if out is None:
             out = torch.empty((tokens, heads, d), dtype=q.dtype, device=self.device)
         else:
@@ -281,11 +293,31 @@ class KVCache:
         need = self._need[1]
         work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         qs = q.stride()
+        if mask is not None:
+            _check("bqd_kv_attend_masked", self._lib.bqd_kv_attend_masked(
+                self._ref, self._layer(layer), q.data_ptr(), qs[0], qs[1], kind, heads, at, tokens, max_new, max_len,
+                self._scale if scale is None else scale, window, mask.data_ptr(), mask.shape[1],
+                None if depth is None else depth.data_ptr(), out.data_ptr(), lse.data_ptr(),
+                work.data_ptr() if need else None, need, self._stream()))
+            return out, lse
         _check("bqd_kv_attend", self._attend(
             self._ref, self._layer(layer), q.data_ptr(), qs[0], qs[1], kind, heads, at, tokens, max_new, max_len,
             self._scale if scale is None else scale, window, out.data_ptr(), lse.data_ptr(),
             work.data_ptr() if need else None, need, self._stream()))
         return out, lse
+
+    def _masks(self, mask, depth, tokens, window):
+        """Checks a masked call's tensors."""
+        if mask is None:
+            raise ValueError("depth: belongs to a mask")
+        words = mask.shape[1] if getattr(mask, "dim", lambda: 0)() == 2 else 0
+        if not 1 <= words <= MASK_WORDS:
+            raise ValueError(f"mask: must be int64 [tokens, words] with words in [1, {MASK_WORDS}]")
+        _dense(mask, "mask", torch.int64, (tokens, words), self.device)
+        if depth is not None:
+            _dense(depth, "depth", torch.int32, (tokens,), self.device)
+        elif window:
+            raise ValueError("depth: a window needs the queries' positions")
 
     def attend_workspace(self, q_heads: int, tokens: int, max_new: int, max_len: int = 0, window: int = 0) -> int:
         """Bytes of scratch that ``attend`` takes for such a call (bqd_kv_attend_workspace)."""
@@ -341,6 +373,26 @@ class KVCache:
                 return self.truncate(keep, out=out)
         return self.fork(torch.arange(self.rows, dtype=torch.int32, device=self.device), keep, out=out)
 
+    def accept(self, path, starts=None, *, out=None, stream=None):
+        """Of each row's last tokens (starts[r + 1] - starts[r] of them, or one) keeps those that
+        its path names, in every layer: token number path[r, k] of them becomes number k
+        (bqd_kv_accept).  path int32 [rows, width] rises and ends before the first entry that does
+        not, as ``spec_tree_verify`` returns it.  Returns the cache that takes this one's place;
+        pages that no row lists any more are free."""
+        if getattr(path, "dim", lambda: 0)() != 2 or path.shape[1] < 1:
+            raise ValueError("path must be an int32 tensor [rows, width]")
+        _dense(path, "path", torch.int32, (self.rows, path.shape[1]), self.device)
+        if starts is not None:
+            _dense(starts, "starts", torch.int32, (self.rows + 1,), self.device)
+        on = self._on(stream)
+        if on is not None:
+            with on:
+                return self.accept(path, starts, out=out)
+        new = self._sibling(self.rows, out)
+        _check("bqd_kv_accept", self._lib.bqd_kv_accept(self._ref, new._ref, path.data_ptr() or None, path.shape[1],
+                                                        None if starts is None else starts.data_ptr(), self._stream()))
+        return new
+
     def compact(self, *, out=None, work=None, stream=None):
         """Moves the live pages to the low end of the pool (bqd_kv_compact).  Returns the cache
         that takes this one's place and an int32 [1] count of the pages that moved.  ``work``
@@ -380,3 +432,4 @@ class KVCache:
 kv_append, kv_attend, kv_reserve = KVCache.append, KVCache.attend, KVCache.reserve
 kv_attend_workspace = KVCache.attend_workspace
 kv_fork, kv_compact, kv_copy_pages = KVCache.fork, KVCache.compact, KVCache.copy_pages
+kv_accept, kv_attend_masked = KVCache.accept, KVCache.attend  # (the masked form: attend with a mask)

@@ -1,8 +1,10 @@
 /*
  * bqd.h -- C ABI of libbqd: the decode-time low-bit quantized matrix-vector
  * product (QMV), its prefill matrix product (QMM), the speculative-decoding
- * verification kernel and a paged 8-bit KV cache (append, attention over it,
- * page operations), on GB300 (sm_103a).
+ * verification kernel, a paged 8-bit KV cache (append, attention over it, page
+ * operations) and what a step with a tree of drafts needs beside them (norm and
+ * rotation of queries and keys, attention and verification of a tree, acceptance
+ * in the cache, log probabilities), on GB300 (sm_103a).
  *
  * Page defining the operations: "oMLX Bonsai 自定义内核:Qwen 系列快速 QMV 路径
  * 完整解析" (oMLX Bonsai custom kernels: the fast QMV path for the Qwen
@@ -69,8 +71,9 @@ enum {
 /* weight formats */
 enum { BQD_FMT_AFFINE1 = 1, BQD_FMT_AFFINE2 = 2, BQD_FMT_T5 = 3 };
 
-/* element types: F16 and F32 for bqd_spec_decode_verify's logits, F16 and BF16
- * for the tensors of the KV cache's entry points */
+/* element types: F16 and F32 for bqd_spec_decode_verify's logits, all three for
+ * those of bqd_spec_tree_verify and bqd_token_logprobs, F16 and BF16 for the
+ * tensors of the KV cache's entry points and of bqd_qk_norm_rope */
 enum { BQD_DTYPE_F16 = 1, BQD_DTYPE_F32 = 2, BQD_DTYPE_BF16 = 3 };
 
 /* code types of the KV cache */
@@ -210,6 +213,106 @@ int bqd_spec_decode_verify(const void *logits, int dtype, const int32_t *draft, 
                            bqd_stream_t stream);
 
 /*
+ * A tree of drafts for each of `rows` sequences.  Row r's nodes are tokens
+ * starts[r] .. starts[r+1]-1 of a ragged batch; parents[i] is the row's own index
+ * of node i's parent, which comes before it: any value outside [0, i) makes node
+ * i a root.  Nodes of no row are left as they are.
+ *   parents    device int32 [tokens];  starts  device int32 [rows + 1]
+ *   words      64-bit words of a node's mask, 1 .. BQD_TREE_MAX_WORDS
+ *   mask       device [tokens, words] or NULL: bit j of node i's mask (bit j % 64 of
+ *              word j / 64) is set where node j of the row is an ancestor of node i
+ *              or i itself; nodes past 64 words have no bit
+ *   depth      device int32 [tokens] or NULL: ancestors of the node
+ *   base       device int32 [rows], or NULL without positions
+ *   positions  device int32 [tokens] or NULL: base[r] + depth
+ */
+#define BQD_TREE_MAX_WORDS 16
+int bqd_tree_mask(const int32_t *parents, const int32_t *starts, int64_t rows, int64_t tokens, int words,
+                  const int32_t *base, uint64_t *mask, int32_t *depth, int32_t *positions, bqd_stream_t stream);
+
+/*
+ * Greedy verification of such trees.  With t[i] = argmax over v of logits[i, v]
+ * (ties: the smallest v; NaN entries are never chosen; a row of NaNs gives -1), the
+ * walk starts at the row's node 0, which is taken as it is, and goes on from a node
+ * i to its lowest child whose drafted token is t[i], as long as there is one.
+ *   logits      device [tokens, V] of `dtype` (F16, BF16 or F32), rows row_stride
+ *               elements apart, aligned to its element size; row i scores the token
+ *               that follows node i
+ *   drafted     device int32 [tokens]: the nodes' tokens; ids outside [0, V) never
+ *               match
+ *   max_path    nodes of a path at most, >= 1: the walk ends there
+ *   accepted    device int32 [rows]: nodes of the path without node 0 (0 for a row
+ *               without nodes)
+ *   next_token  device int32 [rows]: t of the path's last node (-1 for a row without
+ *               nodes)
+ *   path        device int32 [rows, max_path]: the path's nodes, then -1
+ *   argmax_out  device int32 [tokens]: t, of every node (also the call's scratch)
+ * tokens <= 2^28, 1 <= V <= 2^31 - 1024.  rows == 0 launches nothing.
+ */
+int bqd_spec_tree_verify(const void *logits, int dtype, int64_t row_stride, int64_t V, const int32_t *drafted,
+                         const int32_t *parents, const int32_t *starts, int64_t rows, int64_t tokens, int max_path,
+                         int32_t *accepted, int32_t *next_token, int32_t *path, int32_t *argmax_out,
+                         bqd_stream_t stream);
+
+/*
+ * Log probabilities under softmax(logits[r, :]), for each row r:
+ *   logprob[r]   of tokens[r]; -infinity for an id outside [0, V)
+ *   entropy[r]   -sum p log p (natural logarithm)
+ *   rank[r]      entries before tokens[r]: larger, or equal with a lower index; -1 for
+ *                an id outside [0, V)
+ *   top_ids, top_logprobs [r, k], k < top: the largest entries in this order
+ * NaN counts as -infinity, which has probability 0: it is never listed (the list
+ * ends with ids of -1 at -infinity), and a row of nothing else gives -infinity and an
+ * entropy of 0.  A row with +infinity has no distribution: its log probabilities
+ * and entropy are NaN, its ids and rank hold.  Sums are fp32.
+ *   logits  device [rows, V] of `dtype` (F16, BF16 or F32), rows row_stride elements
+ *           apart, aligned to its element size
+ *   tokens  device int32 [rows]; NULL without logprob and rank
+ *   top     0 .. BQD_MAX_TOP
+ *   logprob, entropy, rank [rows], top_ids, top_logprobs [rows, top]: device fp32 and
+ *           int32, each may be NULL
+ */
+#define BQD_MAX_TOP 32
+int bqd_token_logprobs(const void *logits, int dtype, int64_t row_stride, int64_t rows, int64_t V, const int32_t *tokens,
+                       int top, float *logprob, float *entropy, int32_t *rank, int32_t *top_ids, float *top_logprobs,
+                       bqd_stream_t stream);
+
+/*
+ * Norm of each query and key head and the rotation by position, in one pass:
+ *   y = x w / sqrt(mean(x^2) + eps) over the head's head_dim values (norm != 0),
+ * then the pairs j < rotary_dim / 2 of y, (j, j + rotary_dim / 2) or (2 j, 2 j + 1)
+ * (interleaved != 0), become amplitude (a cos t - b sin t, a sin t + b cos t) with t =
+ * positions[token] * inv_freq[j].  Values past rotary_dim are not rotated.  All of
+ * it in fp32 (squares sum to less than 2^128), rounded once.
+ *   q_weight, k_weight  device [head_dim] of weight_dtype (the tensors' type, or F32),
+ *                       or NULL: ones
+ *   freqs       device [rotary_dim / 2]: inv_freq[j] / (2 pi) * 2^64, rounded, modulo
+ *               2^64, so that a product with a position is the angle modulo a turn
+ *   head_dim    64, 128 or 256;  rotary_dim  a multiple of 16 up to head_dim; 0: none
+ */
+typedef struct bqd_qk_rope {
+    const void *q_weight, *k_weight;
+    const uint64_t *freqs;
+    int32_t head_dim, rotary_dim, weight_dtype, interleaved, norm, reserved; /* reserved: 0 */
+    float eps, amplitude; /* eps > 0 (with norm), amplitude finite */
+} bqd_qk_rope;
+
+/*
+ * q, k, q_out, k_out: device [tokens, heads, head_dim] of `dtype` (F16 or BF16),
+ * each with strides of token and head in elements; head_dim is contiguous, and no two
+ * heads of an output share memory.  16-byte aligned bases with strides of multiples
+ * of 8 take 16-byte accesses, others element accesses.  An output may be its input
+ * (the same base and strides); any other overlap is not allowed.  k_heads == 0 (or
+ * q_heads == 0): no k (no q).
+ *   positions   device int32 [tokens], of any value; NULL with rotary_dim == 0
+ */
+int bqd_qk_norm_rope(const bqd_qk_rope *plan, const void *q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
+                     const void *k, int64_t k_token_stride, int64_t k_head_stride, int k_heads, int dtype,
+                     const int32_t *positions, int64_t tokens, void *q_out, int64_t q_out_token_stride,
+                     int64_t q_out_head_stride, void *k_out, int64_t k_out_token_stride, int64_t k_out_head_stride,
+                     bqd_stream_t stream);
+
+/*
  * Paged 8-bit KV cache.  The page this library follows stops at the linear
  * layers and the verification step; the cache below is what a decode step
  * reads and writes between the k/v projections and the o projection.
@@ -325,6 +428,25 @@ int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q, int64_t q
                   void *work, int64_t work_bytes, bqd_stream_t stream);
 
 /*
+ * The same for a tree of drafted tokens, or any other mask over a row's last tokens.
+ * With n = starts[r+1] - starts[r] (1 without starts), every query of row r sees the
+ * tokens before the row's last n, j < lens[r] - n, and of those the ones whose bit is
+ * set in its mask: token lens[r] - n + j where bit j % 64 of word j / 64 is set (itself
+ * only where its own bit is; bits at or past n are not read, and tokens past 64 words
+ * are seen by none).  A query without any key gives 0 and -infinity.
+ *   mask    device [tokens, words], words 1 .. BQD_TREE_MAX_WORDS (bqd_tree_mask)
+ *   depth   device int32 [tokens]: with a window, query i is at position p = lens[r] - n
+ *           + depth[i] (cut to [0, n)) and sees of the tokens before the last n only
+ *           j > p - window; the mask alone decides on the last n.  NULL without one
+ * bqd_kv_attend_workspace serves both.
+ */
+int bqd_kv_attend_masked(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride,
+                         int64_t q_head_stride, int dtype, int q_heads, const int32_t *starts, int64_t tokens,
+                         int64_t max_new, int64_t max_len, float scale, int64_t window, const uint64_t *mask, int words,
+                         const int32_t *depth, void *out, float *lse, void *work, int64_t work_bytes,
+                         bqd_stream_t stream);
+
+/*
  * Room for counts[r] more tokens in each row (counts == NULL: one for each
  * row that is not empty).  lens grows, table gets the new pages (free pages,
  * lowest index first, in the order of the rows and of their tokens) and refs
@@ -354,6 +476,26 @@ int bqd_kv_reserve(const bqd_kv_cache *cache, const int32_t *counts, int32_t *ba
  */
 int bqd_kv_fork(const bqd_kv_cache *from, const bqd_kv_cache *to, const int32_t *parents, const int32_t *keep,
                 bqd_stream_t stream);
+
+/*
+ * Acceptance of a path through each row's last tokens.  Row r's last n = starts[r+1]
+ * - starts[r] tokens (starts == NULL: its last one) are nodes; it keeps those that its
+ * path names, in every layer: the token at position lens[r] - n + path[r, k] moves to
+ * lens[r] - n + k.  `to` gets the table, lens and refs that follow, as from
+ * bqd_kv_fork: rows end behind what they keep, and pages that no row lists any more
+ * are free.  Rows without nodes stay as they are.
+ * A 16-token block that gets tokens takes s', the largest scale of the tokens that it
+ * then holds; codes of another scale s become rnd(fp32(fp32(code * s) * fp32(1 / s'))),
+ * the others keep their bits.
+ *   path    device int32 [rows, width]: nodes in rising order, as bqd_spec_tree_verify
+ *           gives them; a path ends before the first entry that does not rise or is
+ *           outside [0, n)
+ * The blocks are changed in place: as for bqd_kv_append, no other row (of `from`, or
+ * of a cache that shares the pools) may list a page that gets tokens.  `from` and `to`
+ * as for bqd_kv_fork, with the same number of rows.
+ */
+int bqd_kv_accept(const bqd_kv_cache *from, const bqd_kv_cache *to, const int32_t *path, int width,
+                  const int32_t *starts, bqd_stream_t stream);
 
 /*
  * Compaction: with L live pages (refs > 0), the k-th live page at an index >=
