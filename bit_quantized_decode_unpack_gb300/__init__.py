@@ -344,7 +344,7 @@ def device_status(stream=None) -> int:
 
 from . import drafts, kv_cache, logprobs, rope  # noqa: E402
 from .kv_cache import (KVCache, kv_append, kv_attend, kv_attend_workspace, kv_compact,  # noqa: E402,F401
-                       kv_accept, kv_attend_masked, kv_copy_pages, kv_fork, kv_reserve)
+                       kv_accept, kv_attend_masked, kv_attend_masked_workspace, kv_copy_pages, kv_fork, kv_reserve)
 from .drafts import spec_tree_verify, tree_mask  # noqa: E402,F401
 from .logprobs import TokenLogprobs, token_logprobs  # noqa: E402,F401
 from .rope import QKNormRope, qk_norm_rope, rope_frequencies  # noqa: E402,F401

@@ -94,8 +94,15 @@ int planned_length(const bqd_kv_cache &c, int64_t max_len)
 // against 29 to 31.
 bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 32 : 48); }
 
+// Masked calls of more columns than the few-query kernel takes at once
+bool many_columns(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 8 : 16); }
+
 // bytes of scratch that a call is better with, or 0
-int64_t scratch_need(const AttendArgs &a) { return many_queries(a) ? prefill_workspace(a) : decode_workspace(a); }
+int64_t scratch_need(const AttendArgs &a, bool masked)
+{
+    if (masked) return many_columns(a) ? columns_workspace(a) : decode_workspace(a);
+    return many_queries(a) ? prefill_workspace(a) : decode_workspace(a);
+}
 
 cudaStream_t to_stream(bqd_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
@@ -129,8 +136,10 @@ extern "C" int bqd_kv_append(const bqd_kv_cache *cache, int layer, const void *k
     return launch_append(a, to_stream(stream));
 }
 
-extern "C" int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_heads, int64_t tokens, int64_t max_new,
-                                           int64_t max_len, int64_t window)
+namespace {
+
+int64_t workspace_common(const bqd_kv_cache *cache, int q_heads, int64_t tokens, int64_t max_new, int64_t max_len,
+                         int64_t window, bool masked)
 {
     if (check_cache(cache) != BQD_OK) return 0;
     const bqd_kv_cache &c = *cache;
@@ -149,7 +158,21 @@ extern "C" int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_head
     a.max_len = planned_length(c, max_len);
     a.window = (int)(window < most ? window : 0);
     a.mask = nullptr, a.depth = nullptr, a.words = 0;
-    return scratch_need(a);
+    return scratch_need(a, masked);
+}
+
+}  // namespace
+
+extern "C" int64_t bqd_kv_attend_workspace(const bqd_kv_cache *cache, int q_heads, int64_t tokens, int64_t max_new,
+                                           int64_t max_len, int64_t window)
+{
+    return workspace_common(cache, q_heads, tokens, max_new, max_len, window, false);
+}
+
+extern "C" int64_t bqd_kv_attend_masked_workspace(const bqd_kv_cache *cache, int q_heads, int64_t tokens, int64_t max_new,
+                                                  int64_t max_len, int64_t window)
+{
+    return workspace_common(cache, q_heads, tokens, max_new, max_len, window, true);
 }
 
 namespace {
@@ -190,8 +213,9 @@ int attend_common(const bqd_kv_cache *cache, int layer, const void *q, int64_t q
     a.q_vec = vec_ok(q, q_token_stride, q_head_stride);
     a.mask = mask, a.words = words, a.depth = depth;
     a.work = nullptr;
-    const int64_t need = scratch_need(a);
+    const int64_t need = scratch_need(a, mask != nullptr);
     if (need > 0 && work_bytes >= need) a.work = work;
+    if (mask) return many_columns(a) ? launch_attend_columns(a, to_stream(stream)) : launch_attend_decode(a, to_stream(stream));
     return many_queries(a) ? launch_attend_prefill(a, to_stream(stream)) : launch_attend_decode(a, to_stream(stream));
 }
 

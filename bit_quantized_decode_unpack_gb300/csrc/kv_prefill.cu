@@ -151,16 +151,15 @@ __device__ __forceinline__ float ex2(float x)
 }
 
 // Keys [lo, lo + steps * KT) of a row of length L that any of its queries sees; with a window, that any
-// of the call's queries sees (without one the end stays the row's, so that nothing waits for `starts`;
-// with masks too, since a query may see any of the row's last tokens).
+// of the call's queries sees (without one the end stays the row's, so that nothing waits for `starts`).
 struct RowSteps {
     int lo, steps;
-    __device__ __forceinline__ RowSteps(int L, const Span &span, int window, int KT, bool masked)
+    __device__ __forceinline__ RowSteps(int L, const Span &span, int window, int KT)
     {
         const int first = L - span.rest;  // position of query 0
         lo = window > 0 ? max(0, first + 1 - window) / KT * KT : 0;
         steps = span.n > 0 && L > lo ? (L - lo + KT - 1) / KT : 0;
-        if (window > 0 && !masked) steps = min(steps, max(0, first + span.n - lo + KT - 1) / KT);
+        if (window > 0) steps = min(steps, max(0, first + span.n - lo + KT - 1) / KT);
     }
 };
 
@@ -181,35 +180,7 @@ struct Split {
     int first;      // row of the launch's first query tile: a launch has 65535 tiles at most
 };
 
-// Bits [0, n) of a word, n of any value
-__device__ __forceinline__ uint32_t bits_below(int n)
-{
-    return n <= 0 ? 0u : n >= 32 ? 0xFFFFFFFFu : (1u << n) - 1;
-}
-
-// Which keys a query of a masked call sees: those in (after, first) and, from `first` on (the first of
-// its row's last tokens), those whose bit is set, below `end`.
-struct Seen {
-    const uint32_t *mask;  // 32-bit words of the query's mask
-    int words;             // 0: a row of the tile that is no query
-    int after, first, end;
-    // of keys k .. k + 31
-    __device__ __forceinline__ uint32_t at(int k) const
-    {
-        if (words == 0) return 0u;
-        const int o = k - first;
-        uint32_t v = 0;
-        if (o > -32) {
-            const int w = o >> 5;  // -1: the first word starts inside
-            const uint32_t lo = (unsigned)w < (unsigned)words ? __ldg(mask + w) : 0u;
-            const uint32_t hi = w + 1 < words ? __ldg(mask + w + 1) : 0u;
-            v = __funnelshift_r(lo, hi, o & 31) & bits_below(end - k) & ~bits_below(-o);
-        }
-        return v | (bits_below(-o) & ~bits_below(after + 1 - k));
-    }
-};
-
-template <typename T, int D, int FMT, bool STAGED, bool MASKED>
+template <typename T, int D, int FMT, bool STAGED>
 __global__ void __launch_bounds__(STAGED ? kThreadsStaged : kThreadsF, 1)
 attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const __grid_constant__ CUtensorMap map,
                       unsigned long long wait_ns)
@@ -237,14 +208,14 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
     const int r0 = (int)((gridDim.z - 1 - blockIdx.z) / sp.count) * P::kRows + sp.first;
     if (r0 >= rows) return;
     const int L = a.L.length(row);
-    const RowSteps all_steps(L, span, a.window, KT, MASKED);
+    const RowSteps all_steps(L, span, a.window, KT);
     // rows that the scratch has no room for are the unstaged form's
     if (st.steps > 0 && (all_steps.steps <= st.steps) != STAGED) return;
     const int tiles = min(P::kTiles, (rows - r0 + 127) / 128);
     const int i_min = r0 / a.group, i_max = (min(r0 + P::kRows, rows) - 1) / a.group;
     const int p_first = L - span.rest;  // position of query 0
-    const int hi = MASKED ? L : max(0, p_first + i_max + 1);
-    const int lo = a.window > 0 ? max(0, p_first + (MASKED ? 0 : i_min) + 1 - a.window) : 0;
+    const int hi = max(0, p_first + i_max + 1);
+    const int lo = a.window > 0 ? max(0, p_first + i_min + 1 - a.window) : 0;
     const int k_first = lo / KT * KT, all = hi > k_first ? (hi - k_first + KT - 1) / KT : 0;
     const int from = (int)((int64_t)all * share / sp.count), steps = (int)((int64_t)all * (share + 1) / sp.count) - from;
     const int k_lo = k_first + from * KT;
@@ -300,15 +271,6 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
         if (w < tiles) {
             const bool real = r < rows;
             const int pos = real ? p_first + r / a.group : -1;
-            Seen seen;
-            if constexpr (MASKED) {
-                const int token = span.lo + (real ? r / a.group : 0);
-                seen.mask = reinterpret_cast<const uint32_t *>(a.mask + (int64_t)token * a.words);
-                seen.words = real ? 2 * a.words : 0;
-                seen.first = p_first, seen.end = L, seen.after = -1;
-                if (a.window > 0 && real)
-                    seen.after = p_first + max(0, min(__ldg(a.depth + token), span.rest - 1)) - a.window;
-            }
             const uint32_t q_tile = base + w * (P::kPanels * P::kPanelQ);
             const int row0 = (warp & 3) * 32;  // the warp's rows of the tile
             // ---- q: scaled by 2^-e into fp16 (e of the row's largest magnitude) ----
@@ -378,9 +340,8 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
             mbar_arrive(q_full);
 
             // ---- steps ------------------------------------------------------------
-            // positions of the tile's rows (masked: the last token that each sees, and the last position)
-            const int p_low = MASKED ? p_first - 1 : p_first + (r0 + w * 128) / a.group;
-            const int p_high = MASKED ? L - 1 : p_first + (min(r0 + w * 128 + 128, rows) - 1) / a.group;
+            const int p_low = p_first + (r0 + w * 128) / a.group;                               // positions of
+            const int p_high = p_first + (min(r0 + w * 128 + 128, rows) - 1) / a.group;          // the tile's rows
             const uint32_t o_at = tmem + lanes + (w ? P::kO1 : P::kO0);
             // of a block's raw scores; above 0, so that -inf (masked) stays -inf
             auto factor = [&](float k) { return fmaxf(cs * k, 1.2e-38f); };
@@ -440,19 +401,9 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
 #pragma unroll
                         for (int c = 0; c < kChunks; ++c) ld_wait(sh[c]);
                         if (!whole) {
-                            if constexpr (MASKED) {
 #pragma unroll
-                                for (int c = 0; c < kChunks; ++c) {
-                                    const uint32_t bits = seen.at(k0 + half * kHalf + 32 * c);
-#pragma unroll
-                                    for (int i = 0; i < 32; ++i)
-                                        if (!(bits >> i & 1)) sh[c][i] = 0xFF800000u;  // -inf
-                                }
-                            } else {
-#pragma unroll
-                                for (int i = 0; i < kHalf; ++i)
-                                    if (half * kHalf + i > last || half * kHalf + i <= first) sh[i / 32][i % 32] = 0xFF800000u;  // -inf
-                            }
+                            for (int i = 0; i < kHalf; ++i)
+                                if (half * kHalf + i > last || half * kHalf + i <= first) sh[i / 32][i % 32] = 0xFF800000u;  // -inf
                         }
                         if constexpr (kParts == 1) {
                             float mt = -INFINITY;
@@ -538,12 +489,9 @@ attend_prefill_kernel(const AttendArgs a, const Staged st, const Split sp, const
                         ld32(s_at + 32 * c, s);
                         ld_wait(s);
                         if (!whole) {
-                            uint32_t bits = 0;
-                            if constexpr (MASKED) bits = seen.at(k0 + 32 * c);
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                if (MASKED ? !(bits >> i & 1) : 32 * c + i > last || 32 * c + i <= first)
-                                    s[i] = 0xFF800000u;  // -inf
+                                if (32 * c + i > last || 32 * c + i <= first) s[i] = 0xFF800000u;  // -inf
                         }
                         const float2 va = sc[2 * c], vb = sc[2 * c + 1];
                         const float fa = factor(va.x), fb = factor(vb.x);
@@ -940,7 +888,7 @@ stage_kernel(const AttendArgs a, const Staged st)
     const int j = blockIdx.x >> 1, which = blockIdx.x & 1, head = blockIdx.y, row = blockIdx.z;
     const Span span(a.starts, row, a.tokens, a.max_new);
     const int L = a.L.length(row);
-    const RowSteps all(L, span, a.window, KT, a.mask != nullptr);
+    const RowSteps all(L, span, a.window, KT);
     if (j >= all.steps || all.steps > st.steps) return;
     const int k0 = all.lo + j * KT;
     const int64_t step = ((int64_t)row * a.L.heads + head) * st.steps + j;
@@ -1023,7 +971,6 @@ int64_t most_steps(const AttendArgs &a)
 {
     constexpr int KT = Plan<D>::KT;
     const int64_t capacity = (int64_t)a.L.row_pages << a.L.page_shift, all = (capacity + KT - 1) / KT;
-    if (a.mask) return all;  // a row may have more last tokens than the call computes queries
     return std::min(all, keys_of(a, capacity) / KT + 2);
 }
 
@@ -1085,13 +1032,10 @@ template <typename T, int D, int FMT>
 int launch_t(const AttendArgs &a, cudaStream_t s)
 {
     using P = Plan<D>;
-    const bool masked = a.mask != nullptr;
-    auto direct = masked ? attend_prefill_kernel<T, D, FMT, false, true> : attend_prefill_kernel<T, D, FMT, false, false>;
-    // its tiles are fp16 in either format
-    auto staged = masked ? attend_prefill_kernel<T, D, BQD_KV_INT8, true, true>
-                         : attend_prefill_kernel<T, D, BQD_KV_INT8, true, false>;
-    static bool done[2][2][64] = {};
-    if (!configure(direct, P::kSmem, done[masked][0]) || !configure(staged, P::kSmem, done[masked][1])) return BQD_ERR_CUDA;
+    auto direct = attend_prefill_kernel<T, D, FMT, false>;
+    auto staged = attend_prefill_kernel<T, D, BQD_KV_INT8, true>;  // its tiles are fp16 in either format
+    static bool done[2][64] = {};
+    if (!configure(direct, P::kSmem, done[0]) || !configure(staged, P::kSmem, done[1])) return BQD_ERR_CUDA;
     const int64_t rows = (int64_t)a.max_new * a.group;
     const int64_t q_tiles = (rows + P::kRows - 1) / P::kRows;
     const Scratch<D> plan(a);

@@ -58,14 +58,14 @@ def declare(lib):
     lib.bqd_kv_attend_masked.argtypes = [cp, i32, vp, i64, i64, i32, i32, vp, i64, i64, i64, ctypes.c_float, i64, vp, i32,
                                          vp, vp, vp, vp, i64, vp]
     lib.bqd_kv_accept.argtypes = [cp, cp, vp, i32, vp, vp]
-    lib.bqd_kv_attend_workspace.argtypes = [cp, i32, i64, i64, i64, i64]
+    for f in (lib.bqd_kv_attend_workspace, lib.bqd_kv_attend_masked_workspace):
+        f.argtypes, f.restype = [cp, i32, i64, i64, i64, i64], i64
     lib.bqd_kv_reserve.argtypes = [cp, vp, vp, vp, vp, vp]
     lib.bqd_kv_fork.argtypes = [cp, cp, vp, vp, vp]
     lib.bqd_kv_compact.argtypes = [cp, cp, vp, vp, vp]
     lib.bqd_kv_copy_pages.argtypes = [cp, vp, vp, i64, vp]
     for f in ("append", "attend", "attend_masked", "reserve", "fork", "accept", "compact", "copy_pages"):
         getattr(lib, f"bqd_kv_{f}").restype = i32
-    lib.bqd_kv_attend_workspace.restype = i64
 
 
 def _bind():
@@ -287,9 +287,9 @@ class KVCache:
         else:
             _dense(lse, "lse", torch.float32, (tokens, heads), self.device)
         # scratch, from the allocator's pool of this stream: used by this call alone
-        sizes = (heads, tokens, max_new, max_len, window)
+        sizes = (heads, tokens, max_new, max_len, window, mask is not None)
         if self._need[0] != sizes:
-            self._need = (sizes, self.attend_workspace(*sizes))
+            self._need = (sizes, self.attend_workspace(heads, tokens, max_new, max_len, window, masked=mask is not None))
         need = self._need[1]
         work = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         qs = q.stride()
@@ -319,9 +319,12 @@ class KVCache:
         elif window:
             raise ValueError("depth: a window needs the queries' positions")
 
-    def attend_workspace(self, q_heads: int, tokens: int, max_new: int, max_len: int = 0, window: int = 0) -> int:
-        """Bytes of scratch that ``attend`` takes for such a call (bqd_kv_attend_workspace)."""
-        return self._lib.bqd_kv_attend_workspace(self._ref, q_heads, tokens, max_new, max_len, window)
+    def attend_workspace(self, q_heads: int, tokens: int, max_new: int, max_len: int = 0, window: int = 0, *,
+                         masked: bool = False) -> int:
+        """Bytes of scratch that ``attend`` takes for such a call (bqd_kv_attend_workspace, and
+        bqd_kv_attend_masked_workspace for one with a mask)."""
+        f = self._lib.bqd_kv_attend_masked_workspace if masked else self._lib.bqd_kv_attend_workspace
+        return f(self._ref, q_heads, tokens, max_new, max_len, window)
 
     # ---- pages -------------------------------------------------------------------
 
@@ -432,4 +435,5 @@ class KVCache:
 kv_append, kv_attend, kv_reserve = KVCache.append, KVCache.attend, KVCache.reserve
 kv_attend_workspace = KVCache.attend_workspace
 kv_fork, kv_compact, kv_copy_pages = KVCache.fork, KVCache.compact, KVCache.copy_pages
-kv_accept, kv_attend_masked = KVCache.accept, KVCache.attend  # (the masked form: attend with a mask)
+# (the masked form is attend with a mask)
+kv_accept, kv_attend_masked, kv_attend_masked_workspace = KVCache.accept, KVCache.attend, KVCache.attend_workspace

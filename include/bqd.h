@@ -438,8 +438,11 @@ int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q, int64_t q
  *   depth   device int32 [tokens]: with a window, query i is at position p = lens[r] - n
  *           + depth[i] (cut to [0, n)) and sees of the tokens before the last n only
  *           j > p - window; the mask alone decides on the last n.  NULL without one
- * bqd_kv_attend_workspace serves both.
+ * bqd_kv_attend_masked_workspace gives the bytes of scratch that such a call is better
+ * with, as bqd_kv_attend_workspace does.
  */
+int64_t bqd_kv_attend_masked_workspace(const bqd_kv_cache *cache, int q_heads, int64_t tokens, int64_t max_new,
+                                       int64_t max_len, int64_t window);
 int bqd_kv_attend_masked(const bqd_kv_cache *cache, int layer, const void *q, int64_t q_token_stride,
                          int64_t q_head_stride, int dtype, int q_heads, const int32_t *starts, int64_t tokens,
                          int64_t max_new, int64_t max_len, float scale, int64_t window, const uint64_t *mask, int words,

@@ -107,7 +107,7 @@ def test_equal_shares(n, grp, d, fmt):
     lens, news = [2600, 5, 0, 700, n, 1300], [n, 2, 0, 1, n, n - 1]
     c, q, qd, seen, depth = _case(d, lens, news, "float16", fmt, d, 4, grp, 64, row_pages=4000)
     lib = to_library(c)
-    assert lib.attend_workspace(4 * grp, sum(news), n) > 0
+    assert lib.attend_workspace(4 * grp, sum(news), n, masked=True) > 0
     _compare(c, q, qd, news, "float16", seen)
 
 
@@ -119,7 +119,7 @@ def test_equal_shares_with_a_window(n, grp, d, hk, fmt):
     news = [n] + [int(x) for x in rng.integers(0, n + 1, 23)]
     lens = [max(a, b) for a, b in zip(lens, news)]
     c, q, qd, seen, depth = _case(d, lens, news, "bfloat16", fmt, d, hk, grp, 32, row_pages=600)
-    assert to_library(c).attend_workspace(hk * grp, sum(news), n, 0, 900) > 0
+    assert to_library(c).attend_workspace(hk * grp, sum(news), n, 0, 900, masked=True) > 0
     _compare(c, q, qd, news, "bfloat16", seen, depth=depth, window=900)
 
 
