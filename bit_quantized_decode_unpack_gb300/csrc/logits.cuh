@@ -27,6 +27,29 @@ struct Vec<float> {
         return fmaxf(fmaxf(__uint_as_float(u.x), __uint_as_float(u.y)), fmaxf(__uint_as_float(u.z), __uint_as_float(u.w)));
     }
     static __device__ __forceinline__ float one(const float *p) { return *p; }
+    // values raised to at least kLow; NaN too
+    static constexpr float kLow = -1e38f;
+    static __device__ __forceinline__ uint4 raised(const uint4 &u)
+    {
+        auto f = [](uint32_t w) { return __float_as_uint(fmaxf(__uint_as_float(w), kLow)); };
+        return make_uint4(f(u.x), f(u.y), f(u.z), f(u.w));
+    }
+    // how many values of a few vectors are larger than a bound
+    struct Count {
+        int n = 0;
+        __device__ __forceinline__ void add(const uint4 &u, float bound)
+        {
+            n += __uint_as_float(u.x) > bound, n += __uint_as_float(u.y) > bound;
+            n += __uint_as_float(u.z) > bound, n += __uint_as_float(u.w) > bound;
+        }
+        __device__ __forceinline__ int value() const { return n; }
+    };
+    // the next value below one above -infinity
+    static __device__ __forceinline__ float below(float x)
+    {
+        const uint32_t b = __float_as_uint(x + 0.0f);
+        return b == 0u ? -1.4e-45f : __uint_as_float((b >> 31) ? b + 1 : b - 1);
+    }
 };
 
 template <>
@@ -48,6 +71,38 @@ struct Vec<__half> {
         return fmaxf(f.x, f.y);
     }
     static __device__ __forceinline__ float one(const __half *p) { return __half2float(*p); }
+    // values raised to at least kLow, the lowest finite one; NaN too
+    static constexpr float kLow = -65504.0f;
+    static __device__ __forceinline__ uint4 raised(const uint4 &u)
+    {
+        auto f = [](uint32_t w) {
+            const __half2 m = __hmax2(h(w), h(0xFBFFFBFFu));
+            return *reinterpret_cast<const uint32_t *>(&m);
+        };
+        return make_uint4(f(u.x), f(u.y), f(u.z), f(u.w));
+    }
+    // how many values of a few vectors (up to 32) are larger than a bound: 1 or 0 in each half, an exact sum
+    struct Count {
+        uint32_t n = 0;
+        __device__ __forceinline__ void add(const uint4 &u, float b)
+        {
+            const __half2 y = __float2half2_rn(b);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 m = __hadd2(h(n), __hgt2(h(w[i]), y));
+                n = *reinterpret_cast<const uint32_t *>(&m);
+            }
+        }
+        __device__ __forceinline__ int value() const { return (int)(__low2float(h(n)) + __high2float(h(n))); }
+    };
+    // the next value below one above -infinity
+    static __device__ __forceinline__ float below(float x)
+    {
+        const uint32_t b = __half_as_ushort(__float2half_rn(x + 0.0f));
+        const uint32_t y = b == 0u ? 0x8001u : (b >> 15) ? b + 1 : b - 1;
+        return __half2float(__ushort_as_half((unsigned short)y));
+    }
 };
 
 template <>
@@ -67,6 +122,38 @@ struct Vec<__nv_bfloat16> {
         return fmaxf(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     }
     static __device__ __forceinline__ float one(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+    // values raised to at least kLow (0xFE96); NaN too
+    static constexpr float kLow = -0x1.2cp126f;
+    static __device__ __forceinline__ uint4 raised(const uint4 &u)
+    {
+        auto f = [](uint32_t w) {
+            const __nv_bfloat162 m = __hmax2(h(w), h(0xFE96FE96u));
+            return *reinterpret_cast<const uint32_t *>(&m);
+        };
+        return make_uint4(f(u.x), f(u.y), f(u.z), f(u.w));
+    }
+    // how many values of a few vectors (up to 32) are larger than a bound: 1 or 0 in each half, an exact sum
+    struct Count {
+        uint32_t n = 0;
+        __device__ __forceinline__ void add(const uint4 &u, float b)
+        {
+            const __nv_bfloat162 y = __float2bfloat162_rn(b);
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __nv_bfloat162 m = __hadd2(h(n), __hgt2(h(w[i]), y));
+                n = *reinterpret_cast<const uint32_t *>(&m);
+            }
+        }
+        __device__ __forceinline__ int value() const { return (int)(__low2float(h(n)) + __high2float(h(n))); }
+    };
+    // the next value below one above -infinity
+    static __device__ __forceinline__ float below(float x)
+    {
+        const uint32_t b = __bfloat16_as_ushort(__float2bfloat16_rn(x + 0.0f));
+        const uint32_t y = b == 0u ? 0x8001u : (b >> 15) ? b + 1 : b - 1;
+        return __uint_as_float((uint32_t)y << 16);
+    }
 };
 
 // Part `part` of `parts` of a row of n values: 16-byte vectors [q0, q1) behind the first

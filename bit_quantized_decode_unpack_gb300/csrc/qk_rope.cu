@@ -11,13 +11,14 @@
 // an error below 2^-64 position turns: no position is too far.  The upper 32 bits
 // go to sincospi, whose argument is then off by at most 2^-25 turns.
 //
-// Layout.  A lane has 16 values of a head: 8 from each half of the pairs, so both
-// members of its 8 pairs are its own and the only exchange is the sum of squares
-// over D / 16 lanes.  A warp takes 512 / D heads at a time and keeps the sines and
-// cosines of one token for all of its heads.  Few tokens: a token's heads are
-// spread over warps, each computes the angles again (latency counts).  Many: one
-// warp takes a token, with the next heads' loads in flight while these are computed.
-// Bound by memory, 2 bytes read and 2 written a value.
+// Layout.  A lane has 16 values of a head, the members a and b of 8 pairs (what is not
+// rotated counts as pairs too), so the only exchange is the sum of squares over D / 16
+// lanes.  A warp takes 512 / D heads at a time and several such groups of one token, the
+// next two groups' loads in flight while one is computed.  Its lanes share the token's
+// angles out among them and exchange them once, weights are folded into the sines and
+// cosines, and two values go through each fp32 instruction:
+//   y_a = r (a (w_a cos) - b (w_b sin)),  y_b = r (a (w_a sin) + b (w_b cos)),
+// r the reciprocal root.  Bound by memory, 2 bytes read and 2 written a value.
 #include <algorithm>
 #include <cmath>
 
@@ -29,6 +30,7 @@ namespace {
 using kv::Half2Of;
 
 constexpr int kWarpsR = 4;
+constexpr int kAhead = 2;  // head groups in flight of a warp: with 24 warps an SM, 82 us for 470 MB; 4 and 16 warps: 101
 
 struct RopeParams {
     const void *x[2];            // q, k
@@ -39,7 +41,7 @@ struct RopeParams {
     const uint64_t *freqs;
     int heads[2];
     int64_t units;               // warps with work
-    int parts, each;             // warps of a token, head groups of a warp
+    int parts, q_parts, each;    // warps of a token, those with heads of q, head groups of a warp
     int pair_lanes;              // rotary / 16: lanes of a head whose values are rotated
     int rotary;
     bool norm, w_f32;
@@ -75,8 +77,37 @@ __device__ __forceinline__ void store8(unsigned short *p, const uint4 &v)
     }
 }
 
+__device__ __forceinline__ uint64_t two(float a, float b)
+{
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+__device__ __forceinline__ float2 untwo(uint64_t x)
+{
+    float2 f;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(f.x), "=f"(f.y) : "l"(x));
+    return f;
+}
+
+// two fp32 operations in one instruction, each rounded as by itself
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
 template <typename T, int D, bool INTERLEAVED, bool VEC>
-__global__ void __launch_bounds__(kWarpsR * 32)
+__global__ void __launch_bounds__(kWarpsR * 32, 6)
 qk_rope_kernel(const RopeParams p)
 {
     using H = Half2Of<T>;
@@ -88,79 +119,122 @@ qk_rope_kernel(const RopeParams p)
     const int64_t token = unit / p.parts;
     const int part = (int)(unit - token * p.parts);
     const int c = lane % kLanes, sub = lane / kLanes;
-    const bool turned = c < p.pair_lanes;
-    // the lane's two runs of 8 values
-    const int e0 = INTERLEAVED ? 16 * c : turned ? 8 * c : p.rotary + 16 * (c - p.pair_lanes);
-    const int e1 = !INTERLEAVED && turned ? e0 + p.rotary / 2 : e0 + 8;
+    // The lane's two runs of 8 values, each next to its neighbours' (whole sectors in each access), and
+    // whether they are rotated.  Interleaved: four pairs a run.  Else the members of eight pairs, first
+    // those of the rotated values, then of the others.
+    const bool in = c < p.pair_lanes;
+    const int e0 = INTERLEAVED || in ? 8 * c : p.rotary + 8 * (c - p.pair_lanes);
+    const int e1 = INTERLEAVED ? D / 2 + 8 * c : e0 + (in ? p.rotary / 2 : (D - p.rotary) / 2);
+    const bool turned0 = INTERLEAVED ? e0 < p.rotary : in, turned1 = INTERLEAVED ? e1 < p.rotary : in;
 
-    const int q_groups = (p.heads[0] + kHeads - 1) / kHeads, k_groups = (p.heads[1] + kHeads - 1) / kHeads;
-    const int g0 = part * p.each, g1 = min(g0 + p.each, q_groups + k_groups);
-    uint4 n0, n1;  // the next group's values
-    auto load = [&](int g) {
-        n0 = n1 = make_uint4(0, 0, 0, 0);
-        if (g >= g1) return;
-        const int which = g >= q_groups, head = (which ? g - q_groups : g) * kHeads + sub;
-        if (head >= p.heads[which]) return;
-        const unsigned short *x = static_cast<const unsigned short *>(p.x[which]) + token * p.xt[which] + head * p.xh[which];
-        n0 = load8<VEC>(x + e0);
-        n1 = load8<VEC>(x + e1);
+    // a warp has heads of q or of k
+    const int which = part >= p.q_parts, g0 = (which ? part - p.q_parts : part) * p.each;
+    const int heads = p.heads[which], groups = min(p.each, (heads + kHeads - 1) / kHeads - g0);
+    const int head = g0 * kHeads + sub;  // of the lane's first group
+    const int64_t x_step = kHeads * p.xh[which], y_step = kHeads * p.yh[which];
+    const unsigned short *x_at = static_cast<const unsigned short *>(p.x[which]) + token * p.xt[which] + head * p.xh[which];
+    unsigned short *y_at = static_cast<unsigned short *>(p.y[which]) + token * p.yt[which] + head * p.yh[which];
+    const int mine = head < heads ? min(groups, (heads - head + kHeads - 1) / kHeads) : 0;  // groups with a head of the lane's
+    uint4 ring[kAhead][2];               // values of the next groups, on their way
+    auto load = [&](int i, uint4 (&n)[2]) {
+        n[0] = n[1] = make_uint4(0, 0, 0, 0);
+        if (i < mine) n[0] = load8<VEC>(x_at + e0), n[1] = load8<VEC>(x_at + e1);
+        x_at += x_step;
     };
-    load(g0);
-
-    float cs[8], sn[8];
-    if (turned) {
-        const int64_t pos = p.positions[token];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint64_t t = (uint64_t)pos * __ldg(p.freqs + 8 * c + i);
-            sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f, &sn[i], &cs[i]);  // 2^-31: half turns
-            cs[i] *= p.amplitude, sn[i] *= p.amplitude;
+    for (int i = 0; i < kAhead; ++i) load(i, ring[i]);
+
+    // lane (sub, c) computes 8 / kHeads of the angles of lanes (., c), and gets the others from there
+    uint64_t cs[4], sn[4];  // two pairs each
+    {
+        constexpr int kMine = 8 / kHeads;
+        float co[kMine], si[kMine];
+        const int64_t pos = p.pair_lanes ? p.positions[token] : 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            co[i] = 1.0f, si[i] = 0.0f;
+            const int pair = sub * kMine + i;  // of the lane's 8
+            if (pair < 4 ? turned0 : turned1) {
+                const int j = !INTERLEAVED ? 8 * c + pair : 4 * c + (pair < 4 ? pair : D / 4 + pair - 4);
+                const uint64_t t = (uint64_t)pos * __ldg(p.freqs + j);
+                sincospif((float)(int32_t)(t >> 32) * 4.656612873077393e-10f, &si[i], &co[i]);  // 2^-31: half turns
+                co[i] *= p.amplitude, si[i] *= p.amplitude;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int s0 = c + kLanes * ((2 * i) / kMine), s1 = c + kLanes * ((2 * i + 1) / kMine);
+            cs[i] = two(__shfl_sync(0xffffffffu, co[(2 * i) % kMine], s0), __shfl_sync(0xffffffffu, co[(2 * i + 1) % kMine], s1));
+            sn[i] = two(__shfl_sync(0xffffffffu, si[(2 * i) % kMine], s0), __shfl_sync(0xffffffffu, si[(2 * i + 1) % kMine], s1));
         }
     }
-    float w[16];
-    int loaded = -1;  // whose weights are in w
-    for (int g = g0; g < g1; ++g) {
-        const int which = g >= q_groups, head = (which ? g - q_groups : g) * kHeads + sub;
-        const uint32_t u[8] = {n0.x, n0.y, n0.z, n0.w, n1.x, n1.y, n1.z, n1.w};
-        load(g + 1);
-        if (loaded != which) {
-            loaded = which;
+    uint64_t ac[4], as[4], bc[4], bs[4];  // w_a cos, w_a sin, w_b cos, - w_b sin
+    {
+        const void *w = p.w[which];
+        auto weight = [&](int e) {
+            return !w ? 1.0f
+                   : p.w_f32 ? __ldg(static_cast<const float *>(w) + e)
+                             : H::f1(__ldg(static_cast<const unsigned short *>(w) + e));
+        };
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int e = i < 8 ? e0 + i : e1 + i - 8;
-                w[i] = !p.w[which] ? 1.0f
-                       : p.w_f32   ? __ldg(static_cast<const float *>(p.w[which]) + e)
-                                   : H::f1(__ldg(static_cast<const unsigned short *>(p.w[which]) + e));
+        for (int i = 0; i < 4; ++i) {
+            // (members of pairs 2i, 2i + 1)
+            const int at = INTERLEAVED ? (i < 2 ? e0 + 4 * i : e1 + 4 * i - 8) : e0 + 2 * i;
+            const uint64_t wa = INTERLEAVED ? two(weight(at), weight(at + 2)) : two(weight(at), weight(at + 1));
+            const uint64_t wb = INTERLEAVED ? two(weight(at + 1), weight(at + 3)) : two(weight(e1 + 2 * i), weight(e1 + 2 * i + 1));
+            ac[i] = mul2(wa, cs[i]), as[i] = mul2(wa, sn[i]), bc[i] = mul2(wb, cs[i]);
+            bs[i] = mul2(mul2(wb, sn[i]), two(-1.0f, -1.0f));
+        }
+    }
+    const bool all = p.rotary == D;  // nothing is left as it is
+    for (int ib = 0; ib < groups; ib += kAhead)
+#pragma unroll
+    for (int slot = 0; slot < kAhead; ++slot) {
+        if (ib + slot >= groups) break;
+        const uint32_t u[8] = {ring[slot][0].x, ring[slot][0].y, ring[slot][0].z, ring[slot][0].w,
+                               ring[slot][1].x, ring[slot][1].y, ring[slot][1].z, ring[slot][1].w};
+        load(ib + slot + kAhead, ring[slot]);
+        uint64_t a[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (INTERLEAVED) {
+                const float2 f = H::f2(u[2 * i]), h = H::f2(u[2 * i + 1]);
+                a[i] = two(f.x, h.x), b[i] = two(f.y, h.y);
+            } else {
+                const float2 f = H::f2(u[i]), h = H::f2(u[4 + i]);
+                a[i] = two(f.x, f.y), b[i] = two(h.x, h.y);
             }
         }
-        float x[16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float2 f = H::f2(u[i]);
-            x[2 * i] = f.x, x[2 * i + 1] = f.y;
-        }
+        float r = 1.0f;
         if (p.norm) {
-            float ss = 0.0f;
+            uint64_t s2 = two(0.0f, 0.0f);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 0; i < 4; ++i) s2 = fma2(b[i], b[i], fma2(a[i], a[i], s2));
+            const float2 f = untwo(s2);
+            float ss = f.x + f.y;
 #pragma unroll
             for (int o = 1; o < kLanes; o <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float r = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = x[i] * r * w[i];
+            r = rsqrtf(fmaf(ss, 1.0f / D, p.eps));
         }
-        if (turned) {
+        const uint64_t rr = two(r, r);
+        float ya[8], yb[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                float &a = INTERLEAVED ? x[2 * i] : x[i], &b = INTERLEAVED ? x[2 * i + 1] : x[8 + i];
-                const float ya = fmaf(a, cs[i], -b * sn[i]), yb = fmaf(a, sn[i], b * cs[i]);
-                a = ya, b = yb;
-            }
+        for (int i = 0; i < 4; ++i) {
+            uint64_t x = mul2(a[i], ac[i]), y = mul2(b[i], bc[i]);
+            // (what is not rotated stays apart: an infinity would meet a sine of 0)
+            if (all || (i < 2 ? turned0 : turned1)) x = fma2(b[i], bs[i], x), y = fma2(a[i], as[i], y);
+            const float2 fx = untwo(mul2(x, rr)), fy = untwo(mul2(y, rr));
+            ya[2 * i] = fx.x, ya[2 * i + 1] = fx.y, yb[2 * i] = fy.x, yb[2 * i + 1] = fy.y;
         }
-        if (head >= p.heads[which]) continue;
-        unsigned short *y = static_cast<unsigned short *>(p.y[which]) + token * p.yt[which] + head * p.yh[which];
-        store8<VEC>(y + e0, make_uint4(H::pack(x[0], x[1]), H::pack(x[2], x[3]), H::pack(x[4], x[5]), H::pack(x[6], x[7])));
-        store8<VEC>(y + e1, make_uint4(H::pack(x[8], x[9]), H::pack(x[10], x[11]), H::pack(x[12], x[13]), H::pack(x[14], x[15])));
+        uint32_t v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            v[i] = INTERLEAVED ? H::pack(ya[i], yb[i]) : i < 4 ? H::pack(ya[2 * i], ya[2 * i + 1]) : H::pack(yb[2 * i - 8], yb[2 * i - 7]);
+        if (ib + slot < mine) {
+            store8<VEC>(y_at + e0, make_uint4(v[0], v[1], v[2], v[3]));
+            store8<VEC>(y_at + e1, make_uint4(v[4], v[5], v[6], v[7]));
+        }
+        y_at += y_step;
     }
 }
 
@@ -168,11 +242,14 @@ template <typename T, int D>
 int launch_t(RopeParams &p, int64_t tokens, bool interleaved, bool vec, cudaStream_t s)
 {
     constexpr int kHeads = 512 / D;
-    const int groups = (p.heads[0] + kHeads - 1) / kHeads + (p.heads[1] + kHeads - 1) / kHeads;
-    // a warp takes all of a token's heads once there are 16 warps an SM without splitting them
-    const int64_t warps = (int64_t)sm_count() * 16;
-    p.each = (int)std::max<int64_t>(1, std::min<int64_t>(groups, tokens * groups / warps));
-    p.parts = (groups + p.each - 1) / p.each;
+    const int groups[2] = {(p.heads[0] + kHeads - 1) / kHeads, (p.heads[1] + kHeads - 1) / kHeads};
+    // a warp takes more of a token's head groups once there are 32 warps an SM (two waves) with fewer
+    const int64_t warps = (int64_t)sm_count() * 32, most = std::max(groups[0], groups[1]);
+    p.each = (int)std::max<int64_t>(1, std::min<int64_t>(most, tokens * (groups[0] + groups[1]) / warps));
+    const int64_t shares = (most + p.each - 1) / p.each;
+    p.each = (int)((most + shares - 1) / shares);
+    p.q_parts = (groups[0] + p.each - 1) / p.each;
+    p.parts = p.q_parts + (groups[1] + p.each - 1) / p.each;
     p.units = tokens * p.parts;
     const int64_t grid = (p.units + kWarpsR - 1) / kWarpsR;
     if (grid > 0x7FFFFFFF) return BQD_ERR_INVALID_ARG;

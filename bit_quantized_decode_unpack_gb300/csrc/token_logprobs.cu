@@ -3,9 +3,9 @@
 //
 //   m = max x,  l = sum 2^((x - m) c),  s = sum 2^((x - m) c) (x - m) c,  c = log2 e
 //   log p(x) = (x - m) - ln l,   entropy = ln l - ln 2 s / l
-// Differences from m come first: every term of s has one sign and nothing large
-// cancels.  -infinity and NaN have probability 0: their (x - m) c is raised to a
-// finite value whose exponential is 0.
+// Every term of s has one sign and nothing large cancels.  (x - m) c is one fma, x c -
+// M with M = m c rounded, and the sums are moved to m exactly at the end.  -infinity and
+// NaN have probability 0: they are raised to a finite value whose exponential is 0.
 //
 // A thread keeps its own (m, l, s), in fp32, and rescales when a batch of 64 bytes
 // brings a larger value, which is rare after the first ones.  Rank counts larger
@@ -14,9 +14,9 @@
 //
 // The k most likely.  The pass itself only leaves each group of 4 lanes with its
 // largest value.  The k-th largest of those, tau, is no larger than the row's k-th
-// value, so only groups that reach tau hold candidates, about k of 64: their values
+// value, so only threads that reach tau hold candidates, about k of 256: their values
 // are read again (from L2) and those >= tau ordered by value, then by index.  Where
-// many groups tie at tau (constant rows, rows masked with a type's lowest value) only
+// many threads tie at tau (constant rows, rows masked with a type's lowest value) only
 // larger values are gathered, and the ties are taken in the order of their indices
 // until k are found.  What overflows the list of candidates even so is found one at a
 // time; the result is exact in each case.
@@ -26,7 +26,6 @@
 // 6.5 instructions, one of them an exponential.
 #include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "kv_common.cuh"
 #include "logits.cuh"
@@ -131,42 +130,6 @@ __device__ __forceinline__ float value_of(uint64_t key)
     return __uint_as_float(b ^ ((b >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// how many of a vector's values are larger than x (or equal to it, with EQ)
-template <typename T, bool EQ>
-__device__ __forceinline__ int count(const uint4 &u, float x)
-{
-    if constexpr (sizeof(T) == 2) {
-        // 1 or 0 in each half; a sum of four is exact
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-        if constexpr (std::is_same<T, __half>::value) {
-            const __half2 y = __float2half2_rn(x);
-            __half2 n = __float2half2_rn(0.0f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __half2 h = lg::Vec<T>::h(w[i]);
-                n = __hadd2(n, EQ ? __hge2(h, y) : __hgt2(h, y));
-            }
-            return (int)(__low2float(n) + __high2float(n));
-        } else {
-            const __nv_bfloat162 y = __float2bfloat162_rn(x);
-            __nv_bfloat162 n = __float2bfloat162_rn(0.0f);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const __nv_bfloat162 h = lg::Vec<T>::h(w[i]);
-                n = __hadd2(n, EQ ? __hge2(h, y) : __hgt2(h, y));
-            }
-            return (int)(__low2float(n) + __high2float(n));
-        }
-    } else {
-        float v[4];
-        lg::Vec<T>::values(u, v);
-        int n = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) n += EQ ? v[i] >= x : v[i] > x;
-        return n;
-    }
-}
-
 template <typename T>
 __global__ void __launch_bounds__(kThreadsP, 4)
 token_logprobs_kernel(const Params p)
@@ -175,10 +138,10 @@ token_logprobs_kernel(const Params p)
     constexpr int E = X::E, B = 4;  // vectors of a batch
     __shared__ uint64_t list[kList];
     __shared__ uint64_t best[kMaxTop];      // this part's k first, in order
-    __shared__ float group_max[kGroups];
-    __shared__ int hit[kGroups];
+    __shared__ __align__(16) float group_max[kGroups];
+    __shared__ int hit[kThreadsP];
     __shared__ Sums warp_sums[kThreadsP / 32], part_sums;
-    __shared__ int warp_count[kThreadsP / 32], part_count, listed, groups_hit, groups_tied;
+    __shared__ int warp_count[kThreadsP / 32], part_count, listed, threads_hit, threads_tied;
     __shared__ float tau;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int part = p.parts > 1 ? (int)cluster_ctarank() : 0;
@@ -195,70 +158,83 @@ token_logprobs_kernel(const Params p)
     const bool ranked = p.rank && given;
 
     // ---- the pass ----------------------------------------------------------------
-    float m = -INFINITY;
+    // The reference R starts at -kFar and follows m, the largest value so far, in steps of 8 or more;
+    // t = x c - M with M = R c, one rounding each; what M is off from R c, less
+    // than 1 up to there, is taken back at the end
+    constexpr float kFar = X::kLow == -65504.0f ? 6e4f : 5e5f;  // (kLow is far below -kFar)
+    float m = -INFINITY, R = -kFar, M = R * kLog2e;
     uint64_t l2 = two(0.0f, 0.0f), s2 = two(0.0f, 0.0f);
     int before = 0;                         // entries before the token
-    auto raise = [&](float to) {            // the reference m to a larger value
-        if (m > -INFINITY) {
-            const float d = fmaxf((m - to) * kLog2e, -1e30f), f = ex2(d);
-            const uint64_t dd = two(d, d), ff = two(f, f);
-            s2 = mul2(fma2(dd, l2, s2), ff);
-            l2 = mul2(l2, ff);
-        }
-        m = to;
-    };
-    auto single = [&](float v, int i) {
+    const float xt_below = xt == -INFINITY ? xt : X::below(xt);
+    auto rank_single = [&](float v, int i) {
         if (!(v == v)) v = -INFINITY;
-        if (v > m) raise(v);
-        const float t = fmaxf((v - m) * kLog2e, -1e30f), e = ex2(t);
-        l2 = add2(l2, two(e, 0.0f));
-        s2 = fma2(two(e, 0.0f), two(t, 0.0f), s2);
         before += ranked && (v > xt || (v == xt && i < token));
     };
-    auto vector = [&](const uint4 &u) {
-        float x[E];
-        X::values(u, x);
-        const uint64_t mm = two(-m, -m), cc = two(kLog2e, kLog2e);
-#pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            float2 t = untwo(mul2(add2(two(x[i], x[i + 1]), mm), cc));
-            t.x = fmaxf(t.x, -1e30f), t.y = fmaxf(t.y, -1e30f);
-            const uint64_t e = two(ex2(t.x), ex2(t.y));
-            l2 = add2(l2, e);
-            s2 = fma2(e, two(t.x, t.y), s2);
-        }
-    };
-    auto rank_vector = [&](const uint4 &u, int q) {
+    auto rank_vector = [&](typename X::Count &n, const uint4 &u, int q) {
         const int i0 = at.first + q * E;
-        if (i0 > token) {
-            before += count<T, false>(u, xt);
-        } else if (i0 + E <= token) {
-            before += xt == -INFINITY ? E : count<T, true>(u, xt);
+        if (i0 > token || (i0 + E <= token && xt > -INFINITY)) {
+            n.add(u, i0 > token ? xt : xt_below);  // an equal value counts where it is before the token
         } else {
             float x[E];
             X::values(u, x);
 #pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const float v = x[e] == x[e] ? x[e] : -INFINITY;
-                before += v > xt || (v == xt && i0 + e < token);
-            }
+            for (int e = 0; e < E; ++e) rank_single(x[e], i0 + e);
         }
+    };
+    auto raise = [&](float to) {            // the reference, once m is 8 above it
+        const float N = to * kLog2e, d = fmaxf(M - N, -1e30f), f = ex2(d);
+        const uint64_t dd = two(d, d), ff = two(f, f);
+        s2 = mul2(fma2(dd, l2, s2), ff);
+        l2 = mul2(l2, ff);
+        R = to, M = N;
+    };
+    auto vector = [&](const uint4 &u) {
+        float x[E];
+        X::values(X::raised(u), x);
+        const uint64_t mm = two(-M, -M), cc = two(kLog2e, kLog2e);
+#pragma unroll
+        for (int i = 0; i < E; i += 2) {
+            const uint64_t t2 = fma2(two(x[i], x[i + 1]), cc, mm);
+            const float2 t = untwo(t2);
+            const uint64_t e = two(ex2(t.x), ex2(t.y));
+            l2 = add2(l2, e);
+            s2 = fma2(e, t2, s2);
+        }
+    };
+    auto single = [&](float v, int i) {
+        rank_single(v, i);
+        m = fmaxf(m, v);
+        if (m > R + 8.0f) raise(m);
+        const float t = fmaf(fmaxf(v, X::kLow), kLog2e, -M), e = ex2(t);
+        l2 = add2(l2, two(e, 0.0f));
+        s2 = fma2(two(e, 0.0f), two(t, 0.0f), s2);
     };
     if (tid < at.head) single(X::one(row + tid), tid);
     if (tid < at.tail) single(X::one(row + at.tail_at + tid), at.tail_at + tid);
     int q = at.q0 + tid;
-    for (; q + (B - 1) * kThreadsP < at.q1; q += B * kThreadsP) {
+    uint4 next[B];
+    auto load = [&] {
+        if (q + (B - 1) * kThreadsP < at.q1) {
+#pragma unroll
+            for (int j = 0; j < B; ++j) next[j] = __ldg(at.body + q + j * kThreadsP);
+        }
+    };
+    load();
+    while (q + (B - 1) * kThreadsP < at.q1) {
         uint4 u[B];
-        float top[B];
 #pragma unroll
-        for (int j = 0; j < B; ++j) u[j] = __ldg(at.body + q + j * kThreadsP);
-#pragma unroll
-        for (int j = 0; j < B; ++j) top[j] = X::max(u[j]);
-        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-        if (high > m) raise(high);
+        for (int j = 0; j < B; ++j) u[j] = next[j];
+        const int q_now = q;
+        q += B * kThreadsP;
+        load();                             // of the next batch, while this one is summed
+        const float high = fmaxf(fmaxf(X::max(u[0]), X::max(u[1])), fmaxf(X::max(u[2]), X::max(u[3])));
+        m = fmaxf(m, high);
+        if (m > R + 8.0f) raise(m);
         if (ranked && !(high < xt)) {
+            typename X::Count n;
 #pragma unroll
-            for (int j = 0; j < B; ++j) rank_vector(u[j], q + j * kThreadsP);
+            for (int j = 0; j < B; ++j) rank_vector(n, u[j], q_now + j * kThreadsP);
+            before += n.value();
         }
 #pragma unroll
         for (int j = 0; j < B; ++j) vector(u[j]);
@@ -266,16 +242,42 @@ token_logprobs_kernel(const Params p)
     for (; q < at.q1; q += kThreadsP) {
         const uint4 u = __ldg(at.body + q);
         const float high = X::max(u);
-        if (high > m) raise(high);
-        if (ranked && !(high < xt)) rank_vector(u, q);
+        m = fmaxf(m, high);
+        if (m > R + 8.0f) raise(m);
+        if (ranked && !(high < xt)) {
+            typename X::Count n;
+            rank_vector(n, u, q);
+            before += n.value();
+        }
         vector(u);
+    }
+    Sums mine = {m, 0.0f, 0.0f};
+    if (m >= -kFar && m <= kFar) {
+        const float2 l = untwo(l2), s = untwo(s2);
+        const float off = fmaf(m, kLog2e, -M), f = ex2(-off);
+        mine.l = (l.x + l.y) * f;
+        mine.s = fmaf(-off, l.x + l.y, s.x + s.y) * f;
+    } else if (m > -INFINITY) {
+        // a thread whose largest value is far from 0: again, by differences from m (+infinity leaves l = 0)
+        auto one = [&](float v) {
+            const float t = fmaxf((v - m) * kLog2e, -1e30f), e = ex2(t);  // (-infinity and NaN: 0)
+            mine.l += e;
+            mine.s = fmaf(e, t, mine.s);
+        };
+        if (tid < at.head) one(X::one(row + tid));
+        if (tid < at.tail) one(X::one(row + at.tail_at + tid));
+        for (int k = at.q0 + tid; k < at.q1; k += kThreadsP) {
+            float x[E];
+            X::values(__ldg(at.body + k), x);
+#pragma unroll
+            for (int e = 0; e < E; ++e) one(x[e]);
+        }
     }
     const float own_max = m;
 
     // ---- the part's sums -----------------------------------------------------------
     {
-        const float2 l = untwo(l2), s = untwo(s2);
-        Sums a = {m, l.x + l.y, s.x + s.y};
+        Sums a = mine;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) {
             const Sums b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.l, o),
@@ -291,36 +293,46 @@ token_logprobs_kernel(const Params p)
         g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, 2));
         if ((tid & 3) == 0) group_max[tid >> 2] = g;
     }
-    __syncthreads();
-    if (tid == 0) {
-        Sums a = warp_sums[0];
-        int n = warp_count[0];
-        for (int w = 1; w < kThreadsP / 32; ++w) a = join(a, warp_sums[w]), n += warp_count[w];
-        part_sums = a, part_count = n;
-        listed = groups_hit = groups_tied = 0;
-    }
+    if (tid == 0) listed = threads_hit = threads_tied = 0;
     if (tid < kMaxTop) best[tid] = 0;
+    __syncthreads();
+    if (warp == kThreadsP / 32 - 1) {
+        constexpr int kWarpsP = kThreadsP / 32;
+        Sums a = warp_sums[lane % kWarpsP];
+        int n = warp_count[lane % kWarpsP];
+#pragma unroll
+        for (int o = kWarpsP / 2; o > 0; o >>= 1) {
+            const Sums b = {__shfl_xor_sync(0xffffffffu, a.m, o), __shfl_xor_sync(0xffffffffu, a.l, o),
+                            __shfl_xor_sync(0xffffffffu, a.s, o)};
+            a = (lane & o) ? join(b, a) : join(a, b);
+            n += __shfl_xor_sync(0xffffffffu, n, o);
+        }
+        if (lane == 0) part_sums = a, part_count = n;
+    }
 
     // ---- the part's k first ----------------------------------------------------------
     if (p.top > 0) {
         if (tid < kGroups) {
             int n = 0;
             const float g = group_max[tid];
-            for (int i = 0; i < kGroups; ++i) n += group_max[i] > g || (group_max[i] == g && i < tid);
+#pragma unroll 4
+            for (int i = 0; i < kGroups; i += 4) {
+                const float4 o = *reinterpret_cast<const float4 *>(&group_max[i]);
+                n += (o.x > g || (o.x == g && i < tid)) + (o.y > g || (o.y == g && i + 1 < tid)) +
+                     (o.z > g || (o.z == g && i + 2 < tid)) + (o.w > g || (o.w == g && i + 3 < tid));
+            }
             if (n == p.top - 1) tau = g;
         }
         __syncthreads();
         const float t = tau;                // -infinity: every value above it is a candidate
-        if (tid < kGroups) {
-            const bool tied = group_max[tid] == t && t > -INFINITY;
-            if (group_max[tid] > t) hit[atomicAdd(&groups_hit, 1)] = tid;  // (their order is of no consequence)
-            else if (tied) atomicAdd(&groups_tied, 1);
-        }
+        const bool tied = own_max == t && t > -INFINITY;
+        if (own_max > t) hit[atomicAdd(&threads_hit, 1)] = tid;  // (their order is of no consequence)
+        else if (tied) atomicAdd(&threads_tied, 1);
         __syncthreads();
-        const bool few = groups_tied <= 8;  // ties are candidates like others
-        if (few && tid < kGroups && group_max[tid] == t && t > -INFINITY) hit[atomicAdd(&groups_hit, 1)] = tid;
+        const bool few = threads_tied <= 16;  // ties are candidates like others
+        if (few && tied) hit[atomicAdd(&threads_hit, 1)] = tid;
         __syncthreads();
-        const int hits = groups_hit;
+        const int hits = threads_hit, each = at.q1 - at.q0 > 0 ? (at.q1 - at.q0 + kThreadsP - 1) / kThreadsP : 0;
         for (int ties = few; ; ties = 0) {
             auto offer = [&](float v, int i) {
                 if (v > t || (ties && v == t && t > -INFINITY)) {
@@ -330,18 +342,26 @@ token_logprobs_kernel(const Params p)
             };
             if (tid < at.head) offer(X::one(row + tid), tid);
             if (tid < at.tail) offer(X::one(row + at.tail_at + tid), at.tail_at + tid);
-            // a warp takes a group: eight of its lanes' vectors at a time
-            for (int h = warp; h < hits; h += kThreadsP / 32) {
-                const int q_first = at.q0 + hit[h] * 4 + (lane & 3) + (lane >> 2) * kThreadsP;
-#pragma unroll 4
-                for (int q = q_first; q < at.q1; q += 8 * kThreadsP) {
-                    const uint4 u = __ldg(at.body + q);
-                    const float top = X::max(u);
+            // all vectors of the threads that were hit, shared out over all threads, eight on their way
+            const int all = hits * each;
+            for (int i0 = tid; i0 < all; i0 += 8 * kThreadsP) {
+                uint4 u[8];
+                int qs[8];
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int i = i0 + k * kThreadsP;
+                    qs[k] = i < all ? at.q0 + hit[i / each] + i % each * kThreadsP : at.q1;
+                    if (qs[k] < at.q1) u[k] = __ldg(at.body + qs[k]);
+                }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (qs[k] >= at.q1) continue;
+                    const float top = X::max(u[k]);
                     if (top > t || (ties && top == t)) {
                         float x[E];
-                        X::values(u, x);
+                        X::values(u[k], x);
 #pragma unroll
-                        for (int e = 0; e < E; ++e) offer(x[e], at.first + q * E + e);
+                        for (int e = 0; e < E; ++e) offer(x[e], at.first + qs[k] * E + e);
                     }
                 }
             }
@@ -471,9 +491,20 @@ token_logprobs_kernel(const Params p)
     }
     for (int i = tid; i < n; i += kThreadsP) {
         const uint64_t mine = from[i];
-        int above = 0;
-        // keys are apart from each other but for those of no entry, which keep their order
-        for (int k = 0; k < n; ++k) above += from[k] > mine || (mine == 0 && from[k] == 0 && k < i);
+        // the parts' lists are in order: larger keys of each, by bisection (keys are apart from each
+        // other but for those of no entry, which keep their order)
+        const int own = i / p.top;
+        int above = i - own * p.top;
+        for (int k = 0; k < p.parts; ++k) {
+            if (k == own) continue;
+            int lo = 0, hi = p.top;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (from[k * p.top + mid] > mine || (mine == 0 && k < own)) lo = mid + 1;
+                else hi = mid;
+            }
+            above += lo;
+        }
         if (above >= p.top) continue;
         if (p.top_ids) p.top_ids[r * p.top + above] = mine ? (int32_t)(0xFFFFFFFFu - (uint32_t)mine) : -1;
         if (p.top_logprobs) p.top_logprobs[r * p.top + above] = mine ? log_p(value_of(mine)) : -INFINITY;
