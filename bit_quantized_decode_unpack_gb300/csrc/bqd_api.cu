@@ -272,7 +272,7 @@ extern "C" int bqd_device_status(bqd_stream_t stream)
     if (st != BQD_OK) return st;
     st = kv::take_prefill_timeouts(&n6);
     if (st != BQD_OK) return st;
-    st = kv::take_columns_timeouts(&n7);
+    st = kv::take_masked_timeouts(&n7);
     if (st != BQD_OK) return st;
     return (n1 || n2 || n3 || n4 || n5 || n6 || n7) ? BQD_ERR_TIMEOUT : BQD_OK;
 }

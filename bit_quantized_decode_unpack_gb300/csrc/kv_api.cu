@@ -95,12 +95,12 @@ int planned_length(const bqd_kv_cache &c, int64_t max_len)
 bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 32 : 48); }
 
 // Masked calls of more columns than the few-query kernel takes at once
-bool many_columns(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 8 : 16); }
+bool many_rows(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 8 : 16); }
 
 // bytes of scratch that a call is better with, or 0
 int64_t scratch_need(const AttendArgs &a, bool masked)
 {
-    if (masked) return many_columns(a) ? columns_workspace(a) : decode_workspace(a);
+    if (masked) return many_rows(a) ? masked_workspace(a) : decode_workspace(a);
     return many_queries(a) ? prefill_workspace(a) : decode_workspace(a);
 }
 
@@ -215,7 +215,7 @@ int attend_common(const bqd_kv_cache *cache, int layer, const void *q, int64_t q
     a.work = nullptr;
     const int64_t need = scratch_need(a, mask != nullptr);
     if (need > 0 && work_bytes >= need) a.work = work;
-    if (mask) return many_columns(a) ? launch_attend_columns(a, to_stream(stream)) : launch_attend_decode(a, to_stream(stream));
+    if (mask) return many_rows(a) ? launch_attend_masked(a, to_stream(stream)) : launch_attend_decode(a, to_stream(stream));
     return many_queries(a) ? launch_attend_prefill(a, to_stream(stream)) : launch_attend_decode(a, to_stream(stream));
 }
 

@@ -185,7 +185,7 @@ struct AttendArgs {
     const uint64_t *mask;     // [tokens, words]
     const int32_t *depth;     // [tokens]
     int words;
-    void *work;               // scratch of decode_ / prefill_ / columns_workspace bytes, or nullptr
+    void *work;               // scratch of decode_ / prefill_ / masked_workspace bytes, or nullptr
 };
 
 // Request of bqd_kv_append after host validation.
@@ -201,10 +201,10 @@ struct AppendArgs {
 int launch_append(const AppendArgs &a, cudaStream_t s);
 int launch_attend_decode(const AttendArgs &a, cudaStream_t s);
 int launch_attend_prefill(const AttendArgs &a, cudaStream_t s);
-int launch_attend_columns(const AttendArgs &a, cudaStream_t s);  // masked, of more than a few columns
+int launch_attend_masked(const AttendArgs &a, cudaStream_t s);  // masked, of more than a few columns
 int64_t decode_workspace(const AttendArgs &a);   // bytes of their scratch
 int64_t prefill_workspace(const AttendArgs &a);
-int64_t columns_workspace(const AttendArgs &a);
+int64_t masked_workspace(const AttendArgs &a);
 int launch_reserve(const bqd_kv_cache &c, const int32_t *counts, int32_t *base, int32_t *copies, int32_t *status,
                    cudaStream_t s);
 // parents == nullptr: each row its own

@@ -28,38 +28,46 @@ def declare(lib):
     lib.bqd_spec_tree_verify.restype = i32
 
 
+_lib = None
+
+
 def _bind():
-    _kv._bind()
-    if not _LOGITS:
+    """Binds torch, and the library once for all calls."""
+    global _lib
+    if _lib is None:
+        _kv._bind()
         t = _kv.torch
         _LOGITS.update({t.float16: DTYPE_F16, t.bfloat16: DTYPE_BF16, t.float32: DTYPE_F32})
+        _lib = load()
     return _kv.torch
 
 
 def _logits(t):
     """(element type, rows, V, row stride) of logits [rows, V], V contiguous."""
-    if getattr(t, "dim", lambda: 0)() != 2 or not t.is_cuda:
+    shape = getattr(t, "shape", ())
+    if len(shape) != 2 or not t.is_cuda:
         raise ValueError("logits must be a 2-D CUDA tensor [rows, V]")
     kind = _LOGITS.get(t.dtype)
     if kind is None:
         raise ValueError(f"logits: dtype {t.dtype}, expected float16, bfloat16 or float32")
-    (rows, v), (stride, one) = t.shape, t.stride()
+    (rows, v), (stride, one) = shape, t.stride()
     if v < 1 or (v > 1 and one != 1) or (rows > 1 and stride < v):
-        raise ValueError(f"logits: shape {tuple(t.shape)} with strides {tuple(t.stride())}: rows must be contiguous and apart")
-    return kind, rows, v, max(stride, 0)
+        raise ValueError(f"logits: shape {tuple(shape)} with strides {t.stride()}: rows must be contiguous and apart")
+    return kind, rows, v, stride
 
 
 def _tree(parents, starts):
     """(tokens, rows, device) of a batch of trees."""
     torch = _bind()
-    if getattr(parents, "dim", lambda: 0)() != 1 or not parents.is_cuda:
+    tokens, marks = getattr(parents, "shape", ()), getattr(starts, "shape", ())
+    if len(tokens) != 1 or not parents.is_cuda:
         raise ValueError("parents must be an int32 CUDA tensor [tokens]")
-    if getattr(starts, "dim", lambda: 0)() != 1 or starts.shape[0] < 1:
+    if len(marks) != 1 or marks[0] < 1:
         raise ValueError("starts must be an int32 tensor [rows + 1]")
-    tokens, dev = parents.shape[0], parents.device
-    _kv._dense(parents, "parents", torch.int32, (tokens,), dev)
-    _kv._dense(starts, "starts", torch.int32, tuple(starts.shape), dev)
-    return tokens, starts.shape[0] - 1, dev
+    dev = parents.device
+    _kv._dense(parents, "parents", torch.int32, tokens, dev)
+    _kv._dense(starts, "starts", torch.int32, marks, dev)
+    return tokens[0], marks[0] - 1, dev
 
 
 def _here(device, stream):
@@ -73,6 +81,11 @@ def _out(t, name, shape, device, dtype=None):
     if t is None:
         return _kv.torch.empty(shape, dtype=dtype, device=device)
     return _kv._dense(t, name, dtype, shape, device)
+
+
+def _at(t):
+    """Address of an optional tensor."""
+    return None if t is None else t.data_ptr()
 
 
 def tree_mask(parents, starts, *, words: int = 1, base=None, mask=None, depth=None, positions=None, stream=None):
@@ -97,9 +110,9 @@ def tree_mask(parents, starts, *, words: int = 1, base=None, mask=None, depth=No
     depth = _out(depth, "depth", (tokens,), dev)
     if base is not None:
         positions = _out(positions, "positions", (tokens,), dev)
-    p = lambda t: None if t is None else t.data_ptr() or None
-    _check("bqd_tree_mask", load().bqd_tree_mask(p(parents), p(starts), rows, tokens, words, p(base), p(mask), p(depth),
-                                                 p(positions), _kv._raw_stream(dev.index)))
+    _check("bqd_tree_mask", _lib.bqd_tree_mask(
+        parents.data_ptr(), starts.data_ptr(), rows, tokens, words, _at(base), mask.data_ptr(), depth.data_ptr(), _at(positions),
+        _kv._raw_stream(dev.index)))
     return mask, depth, positions
 
 
@@ -129,8 +142,7 @@ def spec_tree_verify(logits, drafted, parents, starts, *, max_path: int, accepte
     next_token = _out(next_token, "next_token", (rows,), dev)
     path = _out(path, "path", (rows, max_path), dev)
     argmax_out = _out(argmax_out, "argmax_out", (tokens,), dev)
-    p = lambda t: t.data_ptr() or None
-    _check("bqd_spec_tree_verify", load().bqd_spec_tree_verify(
-        p(logits), kind, stride, v, p(drafted), p(parents), p(starts), rows, tokens, max_path, p(accepted), p(next_token),
-        p(path), p(argmax_out), _kv._raw_stream(dev.index)))
+    _check("bqd_spec_tree_verify", _lib.bqd_spec_tree_verify(
+        logits.data_ptr(), kind, stride, v, drafted.data_ptr(), parents.data_ptr(), starts.data_ptr(), rows, tokens, max_path,
+        accepted.data_ptr(), next_token.data_ptr(), path.data_ptr(), argmax_out.data_ptr(), _kv._raw_stream(dev.index)))
     return accepted, next_token, path

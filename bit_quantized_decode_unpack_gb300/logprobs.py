@@ -4,7 +4,7 @@ from __future__ import annotations
 import ctypes
 from typing import Any, NamedTuple
 
-from . import _check, load
+from . import _check
 from . import drafts as _drafts
 from . import kv_cache as _kv
 
@@ -51,8 +51,8 @@ def token_logprobs(logits, tokens=None, top: int = 0, *, stream=None) -> TokenLo
     if tokens is not None:
         logprob, rank = empty(rows, dtype=f32, device=dev), empty(rows, dtype=i32, device=dev)
     ids, lps = empty((rows, top), dtype=i32, device=dev), empty((rows, top), dtype=f32, device=dev)
-    p = lambda t: None if t is None else t.data_ptr() or None
-    _check("bqd_token_logprobs", load().bqd_token_logprobs(
-        p(logits), kind, stride, rows, v, p(tokens), top, p(logprob), p(entropy), p(rank), p(ids), p(lps),
-        _kv._raw_stream(dev.index)))
+    at = _drafts._at
+    _check("bqd_token_logprobs", _drafts._lib.bqd_token_logprobs(
+        logits.data_ptr(), kind, stride, rows, v, at(tokens), top, at(logprob), entropy.data_ptr(), at(rank), ids.data_ptr(),
+        lps.data_ptr(), _kv._raw_stream(dev.index)))
     return TokenLogprobs(logprob, entropy, rank, ids, lps)

@@ -111,21 +111,24 @@ class QKNormRope:
         q, k: fp16 or bf16 [tokens, heads, head_dim], any strides of token and head; k may be
         None.  positions: int32 [tokens] (None without rotation).  Outputs are new and dense, or
         q_out and k_out, which may be q and k themselves."""
-        kind = _kv._KINDS.get(getattr(q, "dtype", None))
+        dtype = getattr(q, "dtype", None)
+        kind = _kv._KINDS.get(dtype)
         if kind not in self._kinds:
-            raise ValueError(f"q: dtype {getattr(q, 'dtype', None)}, expected float16 or bfloat16, and that of weights below fp32")
-        tokens = q.shape[0]
-        heads = self._half(q, "q", tokens, q.dtype)
-        k_heads = 0 if k is None else self._half(k, "k", tokens, q.dtype)
+            raise ValueError(f"q: dtype {dtype}, expected float16 or bfloat16, and that of weights below fp32")
+        tokens = q.shape[0] if q.shape else 0
+        heads = self._half(q, "q", tokens, dtype)
+        k_heads = 0 if k is None else self._half(k, "k", tokens, dtype)
+        at = None
         if self.rotary_dim:
             _kv._dense(positions, "positions", _kv.torch.int32, (tokens,), self.device)
+            at = positions.data_ptr()
         if stream is not None or _kv._device() != self._index:
             with _kv._On(self.device, stream):
                 return self(q, k, positions, q_out=q_out, k_out=k_out)
         empty = _kv.torch.empty
         if q_out is None:
-            q_out = empty((tokens, heads, self.head_dim), dtype=q.dtype, device=self.device)
-        elif self._half(q_out, "q_out", tokens, q.dtype) != heads:
+            q_out = empty((tokens, heads, self.head_dim), dtype=dtype, device=self.device)
+        elif self._half(q_out, "q_out", tokens, dtype) != heads:
             raise ValueError(f"q_out: {q_out.shape[1]} heads, expected {heads}")
         if k is None:
             if k_out is not None:
@@ -133,14 +136,14 @@ class QKNormRope:
             ks, kos, k_at, k_to = (0, 0), (0, 0), None, None
         else:
             if k_out is None:
-                k_out = empty((tokens, k_heads, self.head_dim), dtype=q.dtype, device=self.device)
-            elif self._half(k_out, "k_out", tokens, q.dtype) != k_heads:
+                k_out = empty((tokens, k_heads, self.head_dim), dtype=dtype, device=self.device)
+            elif self._half(k_out, "k_out", tokens, dtype) != k_heads:
                 raise ValueError(f"k_out: {k_out.shape[1]} heads, expected {k_heads}")
             ks, kos, k_at, k_to = k.stride(), k_out.stride(), k.data_ptr(), k_out.data_ptr()
         qs, qos = q.stride(), q_out.stride()
         _check("bqd_qk_norm_rope", self._call(
             self._ref, q.data_ptr(), qs[0], qs[1], heads, k_at, ks[0], ks[1], k_heads, kind,
-            positions.data_ptr() if self.rotary_dim else None, tokens, q_out.data_ptr(), qos[0], qos[1], k_to, kos[0], kos[1],
+            at, tokens, q_out.data_ptr(), qos[0], qos[1], k_to, kos[0], kos[1],
             _kv._raw_stream(self._index)))
         return q_out, k_out
 
