@@ -492,16 +492,7 @@ attend_masked_kernel(const AttendArgs a, const Scratch sc, int sms, unsigned lon
             for (int j = streams ? w : 0; j < steps; j += streams ? 2 : 1, ++n) {
                 const int slot = P::kTiles == 1 ? j & 1 : w, phase = P::kTiles == 1 ? j >> 1 : n;
                 const uint32_t s_at = tmem + lanes + (slot ? P::kS1 : 0);
-                // the blocks' scales while S is on its way: shared memory answers slowly while the MMAs
-                // read their operands from it
-                ok = wait(sc_full(j), j / kScaleRing);
-                float2 sr[P::kBlocks];
-#pragma unroll
-                for (int b = 0; b < P::kBlocks; ++b) {
-                    sr[b] = scales[j % kScaleRing][b];
-                    sr[b].x = factor(sr[b].x);
-                }
-                ok = ok && wait(s_full(slot), phase);
+                ok = wait(sc_full(j), j / kScaleRing) && wait(s_full(slot), phase);
                 if (!__all_sync(0xffffffffu, ok)) {
                     ok = false;
                     break;
@@ -526,12 +517,18 @@ attend_masked_kernel(const AttendArgs a, const Scratch sc, int sms, unsigned lon
                 // by too much (the first step, seldom after it) the warp replaces it and computes the part
                 // again.  P takes the place of scores that were read, two values a column.
                 constexpr int kPart = KT / P::kParts, kPartBlocks = kPart / 16, kChunks = kPart / 32;
-#pragma unroll
+                // (a small loop: its code and that of the other roles share the instruction cache)
+#pragma unroll 1
                 for (int part = 0; part < P::kParts; ++part) {
-                    const float2 *v = sr + part * kPartBlocks;
                     uint32_t s[kChunks][32];
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c) ld32(s_at + part * kPart + 32 * c, s[c]);
+                    float2 v[kPartBlocks];  // the blocks' scales, while S is on its way
+#pragma unroll
+                    for (int b = 0; b < kPartBlocks; ++b) {
+                        v[b] = scales[j % kScaleRing][part * kPartBlocks + b];
+                        v[b].x = factor(v[b].x);
+                    }
 #pragma unroll
                     for (int c = 0; c < kChunks; ++c) ld_wait(s[c]);
                     if (!whole) {
