@@ -810,7 +810,7 @@ attend_masked_kernel(const AttendArgs a, const Scratch sc, int sms, unsigned lon
         const uint32_t v_word = desc128_lo(base + P::kOffV, P::kPanelKV);
         auto qk = [&](int j, int tile, int slot) {
             const uint32_t q = q_lo + tile * (P::kTileQ / 16), k = k_word + (j % kStages) * (P::kKV / 16);
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < D / 16; ++s)
                 mma_ss(tmem + (slot ? P::kS1 : 0), q + ((s / 4) * P::kPanelQ + (s % 4) * 32) / 16, hi_word,
                        k + ((s / 4) * P::kPanelKV + (s % 4) * 32) / 16, hi_word, i_qk, s > 0);
@@ -875,10 +875,12 @@ attend_masked_kernel(const AttendArgs a, const Scratch sc, int sms, unsigned lon
             for (int j = 0; j < steps && ok; ++j) {
                 const int w = j & 1;
                 const bool next = j + 2 < steps;
-                ok = tile_of(v_full(j), j) && (!next || tile_of(k_full(j + 2), j + 2)) && pv(j, w, w, j >> 1, j < 2);
+                ok = tile_of(v_full(j), j) && pv(j, w, w, j >> 1, j < 2);
                 if (!ok) break;
                 commit(v_empty(j));
                 if (next) {
+                    ok = tile_of(k_full(j + 2), j + 2);
+                    if (!ok) break;
                     qk(j + 2, 0, w);
                     commit(k_empty(j + 2));
                 } else {
