@@ -1,4 +1,5 @@
 // Host side of the KV cache's C ABI: argument validation, then the launchers.
+#include <algorithm>
 #include <cmath>
 
 #include "kv_common.cuh"
@@ -94,8 +95,25 @@ int planned_length(const bqd_kv_cache &c, int64_t max_len)
 // against 29 to 31.
 bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 32 : 48); }
 
-// Masked calls of more columns than the few-query kernel takes at once
-bool many_rows(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (a.head_dim == 256 ? 8 : 16); }
+// Masked calls: the few-query kernel reads the keys once for each 16 (query, head) columns (8 with
+// head_dim 256), the kernel of 128-row tiles once for each pair of tiles, and starts later.  Times in us
+// with u the million (row, head, key) triples that the call is planned for, measured at 12 to 60 columns,
+// one to 32 rows of 700 to 65001 tokens (few / tiles at 48 columns, head_dim 128: 11 / 23 at one row of 700,
+// 88 / 70 at 8 x 8000, 306 / 188 at 4 x 65001).
+bool many_rows(const AttendArgs &a)
+{
+    struct Cost {
+        double few0, few, tile0, tile, pair;
+    };
+    const Cost c = a.head_dim == 64    ? Cost{8, 32, 17, 71, 114}
+                   : a.head_dim == 128 ? Cost{10, 48, 20, 80, 127}
+                                       : Cost{9, 84, 24, 200, 400};
+    const int64_t columns = (int64_t)a.max_new * a.group, each = a.head_dim == 256 ? 8 : 16, tiles = (columns + 127) / 128;
+    const int64_t keys = a.window > 0 ? std::min<int64_t>(a.max_len, (int64_t)a.window + a.max_new) : a.max_len;
+    const double u = 1e-6 * (double)a.L.rows * a.L.heads * (double)keys;
+    return c.few0 + c.few * u * (double)((columns + each - 1) / each) >
+           c.tile0 + u * (c.pair * (double)(tiles / 2) + c.tile * (double)(tiles % 2));
+}
 
 // bytes of scratch that a call is better with, or 0
 int64_t scratch_need(const AttendArgs &a, bool masked)

@@ -1,6 +1,10 @@
 """Attention over the cache under masks (bqd_kv_attend_masked) against the float64 oracle, with the
 tolerances of the causal attention's tests: the oracle's bound on fp32 scores and fp16 weights, and half a
-unit in the last place of the output type."""
+unit in the last place of the output type.
+
+Two kernels serve masked calls: the few-query one where the call is planned short (by the table's
+capacity, where no length is given) or has few (query, head) rows, and one of 128-row tiles else.
+``tiles`` asserts which one a case is here for: the tile kernel's scratch is over 16 MB, whatever the call."""
 import numpy as np
 import pytest
 
@@ -12,9 +16,15 @@ from test_gpu_draft_trees import _parents
 pytestmark = pytest.mark.gpu
 
 
-def _run(c, q, news, seen, words, depth, window, **kw):
+LONG = 60000  # pages of a row's table: planned long
+
+
+def _run(c, q, news, seen, words, depth, window, tiles=None, **kw):
     import torch
     lib = to_library(c)
+    if tiles is not None:
+        need = lib.attend_workspace(q.shape[1], sum(news), kw.get("max_new", max(news)), kw.get("max_len", 0), window, masked=True)
+        assert (need > 1 << 24) == tiles
     kw.setdefault("max_new", max(news))
     mask = torch.from_numpy(od.mask_words(seen, words)).cuda()
     out, lse = lib.attend(q.cuda(), i32(starts_of(news)), mask=mask, depth=None if depth is None else i32(depth), window=window, **kw)
@@ -60,26 +70,44 @@ SHAPES = [
 @pytest.mark.parametrize("window", [0, 1, 30])
 def test_trees(dtype, fmt, d, hk, grp, pt, lens, news, window):
     c, q, qd, seen, depth = _case(sum(lens) + d, lens, news, dtype, fmt, d, hk, grp, pt)
-    _compare(c, q, qd, news, dtype, seen, depth=depth, window=window)
+    _compare(c, q, qd, news, dtype, seen, depth=depth, window=window, tiles=False)
+
+
+@pytest.mark.parametrize("dtype,fmt,d,hk,grp,pt,lens,news", SHAPES)
+def test_trees_planned_long(dtype, fmt, d, hk, grp, pt, lens, news):
+    """The tile kernel where the rows are more than the few-query kernel takes in two passes (one with heads of 128)."""
+    rows = max(news) * grp
+    c, q, qd, seen, depth = _case(sum(lens) + d, lens, news, dtype, fmt, d, hk, grp, pt, row_pages=LONG)
+    _compare(c, q, qd, news, dtype, seen, depth=depth, tiles=rows > (32 if d == 64 else 16))
+
+
+@pytest.mark.parametrize("d,fmt,dtype", [(64, "e4m3", "bfloat16"), (128, "int8", "float16"), (128, "e4m3", "bfloat16"), (256, "int8", "float16")])
+@pytest.mark.parametrize("window", [1, 70, 900])
+def test_a_window_over_tiles(d, fmt, dtype, window):
+    """Enough rows and heads that even a window's keys are planned for the tile kernel; pairs, single tiles, an empty row."""
+    lens, news = [1500, 64, 0, 700], [64, 60, 0, 33]
+    c, q, qd, seen, depth = _case(d + window, lens, news, dtype, fmt, d, 12, 6, 64)
+    _compare(c, q, qd, news, dtype, seen, depth=depth, window=window, tiles=window == 900 or None)
 
 
 @pytest.mark.parametrize("grp,d", [(1, 64), (4, 128), (2, 256)])
-@pytest.mark.parametrize("window", [0, 200])
-def test_wide_masks(grp, d, window):
+@pytest.mark.parametrize("window,pages", [(0, None), (200, None), (0, LONG)])
+def test_wide_masks(grp, d, window, pages):
     """More than 64 nodes, two to four words, bits that cross them and tiles."""
     news, lens = [150, 65, 200], [400, 65, 231]
-    c, q, qd, seen, depth = _case(7, lens, news, "bfloat16", "int8", d, 1, grp, 32)
+    c, q, qd, seen, depth = _case(7, lens, news, "bfloat16", "int8", d, 1, grp, 32, row_pages=pages)
     _compare(c, q, qd, news, "bfloat16", seen, words=4, depth=depth, window=window)
     # tokens past the words are seen by none
     _compare(c, q, qd, news, "bfloat16", seen, words=2, depth=depth, window=window)
 
 
 @pytest.mark.parametrize("n,grp", [(5, 3), (48, 1), (64, 6)])
-def test_any_mask(n, grp):
+@pytest.mark.parametrize("pages", [None, LONG])
+def test_any_mask(n, grp, pages):
     """Bits of later tokens, rows without a bit, and bits past the row's tokens (not read); with and without a prefix."""
     rng = np.random.default_rng(n)
     news, lens = [n, n, n], [n + 77, n, n]
-    c, q, qd, _, _ = _case(n, lens, news, "float16", "int8", 128, 1, grp, 64)
+    c, q, qd, _, _ = _case(n, lens, news, "float16", "int8", 128, 1, grp, 64, row_pages=pages)
     seen = [set(rng.choice(n + 6, int(rng.integers(0, n)), replace=False).tolist()) for _ in range(3 * n)]
     seen[n:n + 2] = [set(), {n + 1}]
     for i in range(2 * n, 3 * n):
@@ -89,10 +117,11 @@ def test_any_mask(n, grp):
 
 
 @pytest.mark.parametrize("n,grp,d", [(8, 6, 128), (40, 3, 128), (8, 3, 256), (70, 7, 64)])
-def test_a_causal_mask_gives_what_the_causal_call_gives(n, grp, d):
+@pytest.mark.parametrize("pages", [None, 4000])
+def test_a_causal_mask_gives_what_the_causal_call_gives(n, grp, d, pages):
     """Each within its bound of the exact value."""
     news, lens = [n, 3, n - 1], [900, 60, n - 1]
-    c, q, qd, _, _ = _case(n, lens, news, "bfloat16", "int8", d, 2, grp, 64)
+    c, q, qd, _, _ = _case(n, lens, news, "bfloat16", "int8", d, 2, grp, 64, row_pages=pages)
     got, lse = _compare(c, q, qd, news, "bfloat16", [set(range(i + 1)) for m in news for i in range(m)], words=2)
     out, want = to_library(c).attend(q.cuda(), i32(starts_of(news)), max_new=n)
     exact, _, bound, lbound = okv.attend(c, qd, starts_of(news))
@@ -101,13 +130,13 @@ def test_a_causal_mask_gives_what_the_causal_call_gives(n, grp, d):
     assert np.all(np.abs(lse - want.double().cpu().numpy()) <= 2 * lbound + 2.0 ** -21 * np.abs(lse))
 
 
-@pytest.mark.parametrize("n,grp,d,fmt", [(4, 6, 128, "int8"), (7, 7, 64, "e4m3"), (5, 6, 256, "int8")])
+@pytest.mark.parametrize("n,grp,d,fmt", [(4, 4, 128, "int8"), (4, 7, 64, "e4m3"), (2, 6, 256, "int8")])
 def test_equal_shares(n, grp, d, fmt):
     """Few queries planned long, so that shares cut the rows."""
     lens, news = [2600, 5, 0, 700, n, 1300], [n, 2, 0, 1, n, n - 1]
     c, q, qd, seen, depth = _case(d, lens, news, "float16", fmt, d, 4, grp, 64, row_pages=4000)
     lib = to_library(c)
-    assert lib.attend_workspace(4 * grp, sum(news), n, masked=True) > 0
+    assert 0 < lib.attend_workspace(4 * grp, sum(news), n, masked=True) < 1 << 24
     _compare(c, q, qd, news, "float16", seen)
 
 
@@ -119,19 +148,32 @@ def test_equal_shares_with_a_window(n, grp, d, hk, fmt):
     news = [n] + [int(x) for x in rng.integers(0, n + 1, 23)]
     lens = [max(a, b) for a, b in zip(lens, news)]
     c, q, qd, seen, depth = _case(d, lens, news, "bfloat16", fmt, d, hk, grp, 32, row_pages=600)
-    assert to_library(c).attend_workspace(hk * grp, sum(news), n, 0, 900, masked=True) > 0
+    assert 0 < to_library(c).attend_workspace(hk * grp, sum(news), n, 0, 900, masked=True) < 1 << 24
     _compare(c, q, qd, news, "bfloat16", seen, depth=depth, window=900)
 
 
 @pytest.mark.parametrize("d,fmt", [(64, "e4m3"), (128, "int8"), (256, "int8")])
-@pytest.mark.parametrize("window", [0, 900])
-def test_many_queries_behind_long_rows(d, fmt, window):
-    """Several CTAs share a tile's keys; a row longer than planned, and calls without scratch."""
+@pytest.mark.parametrize("hk", [1, 2])
+def test_shares_of_tiles(d, fmt, hk):
+    """Several CTAs share a tile's keys: rows of very different lengths, an empty one, pairs and single tiles.  The same
+    bits every time; a plan that is shorter than the rows; and rows that a CTA does not add up."""
     lens, news = [2500, 0, 9, 1700], [64, 0, 9, 40]
-    c, q, qd, seen, depth = _case(16, lens, news, "bfloat16", fmt, d, 1, 6, 64)
-    got, _ = _compare(c, q, qd, news, "bfloat16", seen, depth=depth, window=window)
-    _compare(c, q, qd, news, "bfloat16", seen, depth=depth, window=window, max_len=1000)
-    np.testing.assert_array_equal(got, _run(c, q, news, seen, 1, depth, window)[0])
+    c, q, qd, seen, depth = _case(16, lens, news, "bfloat16", fmt, d, hk, 6, 64, row_pages=LONG)
+    got, _ = _compare(c, q, qd, news, "bfloat16", seen, tiles=True)
+    np.testing.assert_array_equal(got, _run(c, q, news, seen, 1, depth, 0)[0])
+    _compare(c, q, qd, news, "bfloat16", seen, max_len=1000, tiles=None)
+
+
+@pytest.mark.parametrize("d,grp", [(64, 11), (128, 7), (256, 6)])
+def test_more_rows_than_a_cta_adds_up(d, grp):
+    rng = np.random.default_rng(d)
+    news = [int(n) for n in rng.integers(0, 4, 1030)]
+    lens = [n + int(x) for n, x in zip(news, rng.integers(0, 40, 1030))]
+    lens[5], news[1029] = 700, 3
+    c, q, qd, seen, depth = _case(d, lens, news, "float16", "int8", d, 1, grp, 16, row_pages=4000)
+    lib = to_library(c)
+    assert lib.attend_workspace(grp, sum(news), 3, masked=True) == 0  # nothing is shared
+    _compare(c, q, qd, news, "float16", seen, depth=depth)
 
 
 @pytest.mark.parametrize("d", [64, 128, 256])
@@ -141,7 +183,7 @@ def test_without_scratch(d, window):
     import ctypes
     import torch
     lens, news, hk, grp = [900, 64, 333], [64, 64, 17], 2, 6
-    c, q, qd, seen, depth = _case(3, lens, news, "float16", "int8", d, hk, grp, 64)
+    c, q, qd, seen, depth = _case(3, lens, news, "float16", "int8", d, hk, grp, 64, row_pages=LONG)
     lib = to_library(c)
     qg, starts = q.cuda(), i32(starts_of(news))
     out, lse = torch.empty_like(qg), torch.empty(q.shape[:2], device="cuda")
@@ -155,11 +197,11 @@ def test_without_scratch(d, window):
 
 
 @pytest.mark.parametrize("n,most", [(40, 8), (100, 20), (30, 29)])
-@pytest.mark.parametrize("window", [0, 50])
-def test_more_nodes_than_the_bound(n, most, window):
+@pytest.mark.parametrize("window,pages", [(0, None), (50, None), (0, LONG)])
+def test_more_nodes_than_the_bound(n, most, window, pages):
     """The later queries of a row are not computed; the others see what they saw."""
     news, lens = [n, 3], [300, 40]
-    c, q, qd, seen, depth = _case(4, lens, news, "float16", "int8", 128, 1, 4, 64)
+    c, q, qd, seen, depth = _case(4, lens, news, "float16", "int8", 128, 1, 4, 64, row_pages=pages)
     full, _ = _run(c, q, news, seen, 2, depth, window)
     import torch
     lib = to_library(c)
@@ -179,18 +221,19 @@ def test_wild_depths():
     c, q, qd, seen, _ = _case(5, lens, news, "float16", "int8", 64, 1, 2, 32)
     depth = [-5, 2 ** 31 - 1, -2 ** 31, 3, 7, 0]
     _compare(c, q, qd, news, "float16", seen, depth=depth, window=60)
-    news, lens = [60], [200]
-    c, q, qd, seen, _ = _case(5, lens, news, "float16", "int8", 64, 1, 2, 32)
-    _compare(c, q, qd, news, "float16", seen, depth=depth * 10, window=60)
+    news, lens = [60] * 3, [200, 60, 3000]
+    c, q, qd, seen, _ = _case(5, lens, news, "float16", "int8", 64, 24, 4, 32)
+    _compare(c, q, qd, news, "float16", seen, depth=depth * 30, window=600, tiles=True)
 
 
 @pytest.mark.parametrize("n,grp", [(6, 6), (64, 6)])
 @pytest.mark.parametrize("fmt", ["int8", "e4m3"])
-def test_what_lies_past_the_row_does_not_matter(n, grp, fmt):
+@pytest.mark.parametrize("pages", [None, LONG])
+def test_what_lies_past_the_row_does_not_matter(n, grp, fmt, pages):
     """Stale codes, NaN bytes and NaN scales behind the row's end, on its last page and others."""
     import torch
     lens, news = [n + 39], [n]
-    c, q, qd, seen, depth = _case(6, lens, news, "float16", fmt, 128, 1, grp, 64)
+    c, q, qd, seen, depth = _case(6, lens, news, "float16", fmt, 128, 1, grp, 64, row_pages=pages)
     want, _ = _run(c, q, news, seen, 1, None, 0)
     lib = to_library(c)
     page, used = int(c["table"][0, lens[0] // 64]), lens[0] % 64
