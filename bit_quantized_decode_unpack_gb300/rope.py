@@ -14,13 +14,12 @@ gradients.
 from __future__ import annotations
 
 import ctypes
-from fractions import Fraction
-
 from . import DTYPE_BF16, DTYPE_F16, DTYPE_F32, _check, load
 from . import kv_cache as _kv
 
 HEAD_DIMS = (64, 128, 256)
-_PI = Fraction(31415926535897932384626433832795028841971693993751, 10 ** 49)
+_PI = 31415926535897932384626433832795028841971693993751058209749445923078164  # pi * 10^70
+_TURNS = 10 ** 70 * 2 ** 191 // _PI  # 2^192 / (2 pi)
 _WEIGHTS = {"torch.float16": DTYPE_F16, "torch.bfloat16": DTYPE_BF16, "torch.float32": DTYPE_F32}
 
 
@@ -43,7 +42,12 @@ def declare(lib):
 def rope_frequencies(inv_freq) -> list:
     """Inverse frequencies (radians a position) in turns, as the 64-bit fractions that the kernel
     multiplies by positions: inv_freq / (2 pi) * 2^64, rounded, modulo 2^64."""
-    return [round(Fraction(float(f)) * 2 ** 64 / (2 * _PI)) % 2 ** 64 for f in inv_freq]
+    def turns(f):
+        n, d = float(f).as_integer_ratio()  # d is a power of two
+        shift = 128 + d.bit_length() - 1
+        return (n * _TURNS + (1 << shift - 1) >> shift) % 2 ** 64
+
+    return [turns(f) for f in inv_freq]
 
 
 class QKNormRope:
