@@ -487,6 +487,7 @@ attend_masked_kernel(const AttendArgs a, const Scratch sc, int sms, unsigned lon
             const uint32_t o_at = tmem + lanes + (w ? P::kO1 : P::kO0);
             auto factor = [&](float k) { return fmaxf(cs * k, 1.2e-38f); };  // above 0, so that -inf (masked) stays -inf
             float m = -INFINITY, l = 0.0f;
+            const bool idle = tile_row + row0 >= rows;  // none of the warp's rows is a query
             bool ok = true;
             int n = 0;  // steps of this S (single: of both)
             for (int j = streams ? w : 0; j < steps; j += streams ? 2 : 1, ++n) {
@@ -498,6 +499,11 @@ attend_masked_kernel(const AttendArgs a, const Scratch sc, int sms, unsigned lon
                     break;
                 }
                 fence_after();
+                if (idle) {  // its P may be anything
+#pragma unroll
+                    for (int part = 0; part < P::kParts; ++part) mbar_arrive(p_full(slot, part));
+                    continue;
+                }
                 const int k0 = k_lo + j * KT;
                 const bool whole = k0 + KT <= before && (a.window == 0 || k0 > L - 1 - a.window);
                 auto rescale = [&](float f) {  // O times f

@@ -177,11 +177,11 @@ struct Part {
     }
 };
 
-// CTAs that share a row of n values: until each SM has two, with 4096 values for each at least
-inline int parts_of(int64_t rows, int64_t n, int sms, int most)
+// CTAs that share a row of n values: until there are `ctas` of them, with 4096 values for each at least
+inline int parts_of(int64_t rows, int64_t n, int64_t ctas, int most)
 {
     int parts = 1;
-    while (parts < most && rows * parts < 2 * sms && n >= (int64_t)4096 * 2 * parts) parts *= 2;
+    while (parts < most && rows * parts < ctas && n >= (int64_t)4096 * 2 * parts) parts *= 2;
     return parts;
 }
 
