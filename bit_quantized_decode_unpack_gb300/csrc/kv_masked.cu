@@ -32,6 +32,15 @@
 // the same share length, the one with the least estimated time, and its own place.
 // Shares leave O, m and l in scratch, and a second kernel, launched early, joins
 // them in order.  No atomics: the same bits every time.
+// Bound by neither HBM nor the tensor cores, but by the waits between the roles of a step:
+// the tensor pipe is active 31% of the time, HBM read at 2.8 to 3.0 TB/s (4 x 65001
+// tokens, 8 KV heads of 128, 30 to 126 rows: 186 to 188 us; 252 rows: 286 us).  Which
+// wait decides is not isolated: a conversion takes 1600 to 1900 cycles of a step's 2200 to
+// 3900, yet leaving out its loads or its stores (in a copy) left the period.  The same
+// with the keys as the 128-row operand took 210 us with e4m3 codes (179 here) and 520 for
+// 252 rows; codes loaded straight to registers, two steps ahead, 352.  Softmax warps
+// without a query that skip their steps cost 1 to 2.5% (252 rows 293 us, 126 rows of 256
+// at 4 KV heads 234 -> 240) and gain 1.3% only with heads of 64.
 // Every wait is bounded; on expiry a role stops, what it issued is drained, TMEM is
 // freed, and bqd_device_status reports it.
 #include <algorithm>
@@ -487,7 +496,6 @@ attend_masked_kernel(const AttendArgs a, const Scratch sc, int sms, unsigned lon
             const uint32_t o_at = tmem + lanes + (w ? P::kO1 : P::kO0);
             auto factor = [&](float k) { return fmaxf(cs * k, 1.2e-38f); };  // above 0, so that -inf (masked) stays -inf
             float m = -INFINITY, l = 0.0f;
-            const bool idle = tile_row + row0 >= rows;  // none of the warp's rows is a query
             bool ok = true;
             int n = 0;  // steps of this S (single: of both)
             for (int j = streams ? w : 0; j < steps; j += streams ? 2 : 1, ++n) {
@@ -499,11 +507,6 @@ attend_masked_kernel(const AttendArgs a, const Scratch sc, int sms, unsigned lon
                     break;
                 }
                 fence_after();
-                if (idle) {  // its P may be anything
-#pragma unroll
-                    for (int part = 0; part < P::kParts; ++part) mbar_arrive(p_full(slot, part));
-                    continue;
-                }
                 const int k0 = k_lo + j * KT;
                 const bool whole = k0 + KT <= before && (a.window == 0 || k0 > L - 1 - a.window);
                 auto rescale = [&](float f) {  // O times f
