@@ -22,8 +22,12 @@
 // time; the result is exact in each case.
 //
 // Few rows: the CTAs of a cluster share a row, and the first joins their sums and
-// lists, in order.  No atomics decide a result.  Bound by HBM; per 16-bit value about
-// 6.5 instructions, one of them an exponential.
+// lists, in order.  No atomics decide a result.  2049 rows of 151936 bf16 values: 135 us
+// with 5 alternatives (4610 GB/s, 68% of a measured copy), 112 without; one row with 20
+// alternatives 12 us.  Without alternatives it is near HBM's rate; with them a CTA reads
+// nothing new while it searches, and the whole issues in 62% of the slots (9.4
+// instructions a value).  Bulk prefetches to L2 ahead of the loads: 2049 rows 135 -> 129,
+// but 300 rows 27 -> 34 us, 20 alternatives of fp16 161 -> 170.
 #include <algorithm>
 #include <cmath>
 
