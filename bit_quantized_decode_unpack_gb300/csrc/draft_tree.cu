@@ -3,9 +3,10 @@
 // Row r's nodes are tokens starts[r] .. starts[r + 1] - 1; parents[i] is the row's
 // own index of node i's parent, below i; any other value makes node i a root.
 //
-// bqd_tree_mask: one thread a node walks up to its root and sets the bits of what
-// it passes, from the highest word down, since a parent's index is below its
-// child's.  A chain of n nodes costs n steps of a cached load; drafts are shallow.
+// bqd_tree_mask: one thread a node walks up and sets the bits of what it passes, from
+// the highest word down, since a parent's index is below its child's.  A row's nodes
+// go in groups of 128, in order: a walk that leaves its group takes the rest from what
+// the ancestor there already has, so that it is 128 steps at most, whatever the depth.
 //
 // bqd_spec_tree_verify: t[i] = argmax of node i's logits (ties: the smallest index;
 // NaN is never chosen; -1 for a row of NaNs) in a first kernel, which is bound by
@@ -37,11 +38,14 @@ tree_mask_kernel(const int32_t *parents, const int32_t *starts, int tokens, int 
 {
     const int row = blockIdx.x;
     const Span span(starts, row, tokens, INT_MAX);
-    for (int i = threadIdx.x; i < span.n; i += 128) {
+    for (int i0 = 0; i0 < span.n; i0 += 128) {
+        if (i0 > 0) __syncthreads();  // the groups before are written
+        const int i = i0 + threadIdx.x;
+        if (i >= span.n) continue;    // (of the last group)
         uint64_t *to = mask ? mask + (int64_t)(span.lo + i) * words : nullptr;
         int word = words - 1, above = -1, at = i;
         uint64_t bits = 0;
-        while (at >= 0) {
+        while (at >= i0) {
             ++above;
             if (to && (at >> 6) < words) {
                 while (word > at >> 6) {
@@ -53,11 +57,16 @@ tree_mask_kernel(const int32_t *parents, const int32_t *starts, int tokens, int 
             const int p = __ldg(parents + span.lo + at);
             at = p < at ? max(p, -1) : -1;
         }
+        // an ancestor of an earlier group: its bits lie in words below this group's
+        const int64_t up = at < 0 ? -1 : (int64_t)span.lo + at;
         if (to)
             while (word >= 0) {
-                to[word--] = bits;
+                to[word] = up >= 0 && word < i0 >> 6 ? mask[up * words + word] : bits;
                 bits = 0;
+                --word;
             }
+        if (up >= 0 && depth) above += 1 + depth[up];
+        else if (up >= 0 && positions) above += 1 + positions[up] - base[row];
         if (depth) depth[span.lo + i] = above;
         if (positions) positions[span.lo + i] = base[row] + above;
     }

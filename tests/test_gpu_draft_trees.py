@@ -43,6 +43,37 @@ def test_masks_of_a_chain_and_of_wild_parents():
     assert depth.tolist() == want.tolist()
 
 
+@pytest.mark.parametrize("given", ["mask", "depth", "positions"])
+def test_masks_of_deep_trees_without_the_other_outputs(given):
+    """Walks that leave their group of 128 nodes, each output by itself: nothing may be read from one that is not there."""
+    import ctypes
+    import torch
+    rng = np.random.default_rng(11)
+    news = [700, 1, 129, 1024]
+    parents = _parents(rng, news)
+    parents[-1024:] = [-1] + [i - 1 - (i % 7 == 0 and i > 9) * int(rng.integers(0, 9)) for i in range(1, 1024)]
+    starts, base = starts_of(news), rng.integers(-50, 5000, len(news))
+    seen, want = od.tree_mask(parents, starts)
+    n, p, s, b = len(parents), i32(parents), i32(starts), i32(base)
+    out = torch.full((n, 16) if given == "mask" else (n,), -9, dtype=torch.int64 if given == "mask" else torch.int32, device="cuda")
+    at = {k: out.data_ptr() if k == given else None for k in ("mask", "depth", "positions")}
+    assert bqd.load().bqd_tree_mask(p.data_ptr(), s.data_ptr(), len(news), n, 16, b.data_ptr(), at["mask"], at["depth"],
+                                    at["positions"], torch.cuda.current_stream().cuda_stream) == 0
+    right = {"mask": lambda: od.mask_words(seen, 16), "depth": lambda: want, "positions": lambda: np.repeat(base, news) + want}
+    np.testing.assert_array_equal(out.cpu().numpy(), right[given]())
+
+
+def test_a_chain_of_many_nodes_takes_time_by_its_length():
+    """200000 nodes in one row: 1563 groups of 128 steps, not 2e10 steps."""
+    n = 200_000
+    mask, depth, pos = bqd.tree_mask(i32(range(-1, n - 1)), i32([0, n]), words=2, base=i32([7]))
+    np.testing.assert_array_equal(depth.cpu().numpy(), np.arange(n))
+    np.testing.assert_array_equal(pos.cpu().numpy(), np.arange(n) + 7)
+    i = np.arange(n)[:, None] - 64 * np.arange(2)[None]  # bits 0 .. i of each word
+    want = np.where(i < 0, 0, np.where(i >= 63, -1, (1 << np.clip(i + 1, 0, 63)) - 1)).astype(np.int64)
+    np.testing.assert_array_equal(mask.cpu().numpy(), want)
+
+
 def test_nodes_of_no_row_stay_as_they_are():
     import torch
     mask = torch.full((9, 1), 77, dtype=torch.int64, device="cuda")
