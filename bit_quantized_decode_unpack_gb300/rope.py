@@ -157,4 +157,7 @@ def qk_norm_rope(q, k, positions, inv_freq, *, q_out=None, k_out=None, stream=No
     device wait for the host: keep one where calls repeat)."""
     if getattr(q, "dim", lambda: 0)() != 3:
         raise ValueError("q must be a 3-D tensor [tokens, heads, head_dim]")
+    if stream is not None and q.is_cuda:
+        with _kv._On(q.device, stream):  # the plan's frequencies too: they are freed before the stream has read them
+            return qk_norm_rope(q, k, positions, inv_freq, q_out=q_out, k_out=k_out, **plan)
     return QKNormRope(q.shape[2], inv_freq, device=q.device, **plan)(q, k, positions, q_out=q_out, k_out=k_out, stream=stream)

@@ -156,3 +156,20 @@ def test_refusals():
     assert q.shape == (0, 2, 64) and k.shape == (0, 2, 64)
     a, _ = bqd.qk_norm_rope(x, None, pos, THETA(64))
     assert a.shape == x.shape
+
+
+def test_a_plan_of_one_call_on_another_stream_is_read_before_its_memory_is_used_again():
+    """qk_norm_rope's own plan is gone when the call returns, the kernel perhaps not begun."""
+    import torch
+    rng = np.random.default_rng(5)
+    buf, v = _inputs(rng, 9, 3, 1, 128, "float16")
+    pos, freq, side = np.arange(1000, 1009), THETA(128), torch.cuda.Stream()
+    at = i32(pos)
+    torch.cuda.synchronize()
+    for _ in range(4):
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(20_000_000)
+        q, _ = bqd.qk_norm_rope(buf[:, :3], None, at, freq, stream=side)
+        torch.empty(64, dtype=torch.int64, device="cuda").fill_(0x3333333333333333)  # of the size that the plan's have
+        side.synchronize()
+        _check(q, v[:, :3], pos, freq, "float16", None)
