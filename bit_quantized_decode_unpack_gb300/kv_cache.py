@@ -435,5 +435,9 @@ class KVCache:
 kv_append, kv_attend, kv_reserve = KVCache.append, KVCache.attend, KVCache.reserve
 kv_attend_workspace = KVCache.attend_workspace
 kv_fork, kv_compact, kv_copy_pages = KVCache.fork, KVCache.compact, KVCache.copy_pages
-# (the masked form is attend with a mask)
-kv_accept, kv_attend_masked, kv_attend_masked_workspace = KVCache.accept, KVCache.attend, KVCache.attend_workspace
+kv_accept, kv_attend_masked = KVCache.accept, KVCache.attend  # (the masked form is attend with a mask)
+
+
+def kv_attend_masked_workspace(cache: KVCache, q_heads: int, tokens: int, max_new: int, max_len: int = 0, window: int = 0) -> int:
+    """Bytes of scratch that ``attend`` takes with a mask (bqd_kv_attend_masked_workspace)."""
+    return cache.attend_workspace(q_heads, tokens, max_new, max_len, window, masked=True)

@@ -258,3 +258,13 @@ def test_refusals():
             lib.attend(q, starts, max_new=3, **kw)
     out, _ = lib.attend(q[:0], i32([0, 0, 0]), mask=mask[:0])
     assert out.shape == (0, 4, 64)
+
+
+def test_the_names_of_the_entry_points_are_the_calls():
+    import bit_quantized_decode_unpack_gb300 as bqd
+    c, grp = random_cache(np.random.default_rng(3), [40, 3], heads=2, d=64, pt=16, row_pages=LONG // 16), 4
+    lib = to_library(c)
+    for args in [(2 * grp, 22, 20), (2 * grp, 22, 20, 900, 100), (2 * grp, 2, 1, 64)]:
+        assert bqd.kv_attend_masked_workspace(lib, *args) == lib.attend_workspace(*args, masked=True)
+        assert bqd.kv_attend_workspace(lib, *args) == lib.attend_workspace(*args)
+    assert bqd.kv_attend_masked_workspace(lib, 2 * grp, 22, 20) != bqd.kv_attend_workspace(lib, 2 * grp, 22, 20)
