@@ -375,10 +375,10 @@ token_logprobs_kernel(const Params p)
                 if (!ties && listed <= kList && t > -INFINITY) {
                     const int lo = at.head ? 0 : at.first + at.q0 * E;
                     const int hi = at.tail ? p.V : at.first + at.q1 * E;
-                    for (int i0 = lo; i0 < hi; i0 += 16 * kThreadsP) {
+                    for (unsigned i0 = lo; i0 < (unsigned)hi; i0 += 16 * kThreadsP) {  // (passes 2^31 for the largest V)
                         const int have = listed;
                         if (have >= p.top) break;
-                        const int a = min(hi, i0 + tid * 16), b = min(hi, a + 16);
+                        const int a = (int)min((unsigned)hi, i0 + tid * 16), b = min(hi, a + 16);
                         int n = 0;
                         for (int i = a; i < b; ++i) n += X::one(row + i) == t;
                         int sum = n;

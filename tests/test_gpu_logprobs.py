@@ -173,3 +173,14 @@ def test_refusals():
             bqd.token_logprobs(*args, **kw)
     r = bqd.token_logprobs(x[:0], tok[:0], 4)
     assert r.logprob.shape == (0,) and r.top_ids.shape == (0, 4)
+
+
+def test_ties_at_the_end_of_the_longest_row():
+    """The last indices of the largest V: positions behind the row pass 2^31 in the ordered search for ties."""
+    import torch
+    v = 2 ** 31 - 1024
+    x = torch.full((1, v), -1.0, dtype=torch.bfloat16, device="cuda")
+    x[0, v - 2000:] = 1.0
+    r = bqd.token_logprobs(x, i32([v - 1]), 32)
+    assert r.top_ids[0].tolist() == list(range(v - 2000, v - 1968)) and r.rank.tolist() == [1999]
+    assert bool((r.top_logprobs == r.logprob).all())
