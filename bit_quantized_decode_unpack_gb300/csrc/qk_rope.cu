@@ -20,7 +20,7 @@
 //   y_a = r (a (w_a cos) - b (w_b sin)),  y_b = r (a (w_a sin) + b (w_b cos)),
 // r the reciprocal root.  Bound by memory, 2 bytes read and 2 written a value: 16384
 // tokens of 28 heads of 256 in 82 us for 470 MB (5710 GB/s, 84% of a measured copy); 2049
-// tokens of 56 heads of 128, 12.0 us; 16 tokens 2.8 us, the launch.
+// tokens of 56 heads of 128, 12.1 us; 16 tokens 2.8 us, the launch.
 #include <algorithm>
 #include <cmath>
 
