@@ -435,7 +435,14 @@ class KVCache:
 kv_append, kv_attend, kv_reserve = KVCache.append, KVCache.attend, KVCache.reserve
 kv_attend_workspace = KVCache.attend_workspace
 kv_fork, kv_compact, kv_copy_pages = KVCache.fork, KVCache.compact, KVCache.copy_pages
-kv_accept, kv_attend_masked = KVCache.accept, KVCache.attend  # (the masked form is attend with a mask)
+kv_accept = KVCache.accept
+
+
+def kv_attend_masked(cache: KVCache, q, starts=None, *, mask=None, **how):
+    """``attend`` with a mask (bqd_kv_attend_masked); a call without one is refused, not causal."""
+    if mask is None:
+        raise ValueError("mask: must be int64 [tokens, words] (attend without one is causal)")
+    return cache.attend(q, starts, mask=mask, **how)
 
 
 def kv_attend_masked_workspace(cache: KVCache, q_heads: int, tokens: int, max_new: int, max_len: int = 0, window: int = 0) -> int:
