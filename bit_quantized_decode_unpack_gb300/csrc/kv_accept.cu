@@ -6,6 +6,7 @@
 // rising order, each with all of its tokens in registers before any is written.
 //   s' = max of the scales of the tokens that the block then holds,
 //   code' = code where its scale is s', else rnd(fp32(fp32(code s) fp32(1 / s')))
+// A row with fewer tokens than nodes has a node for each token, from its first one.
 // One warp owns (row, layer, head, K or V): nothing is shared, no atomics.  Blocks
 // before the first entry that moves keep what they have.  A path is a few tokens:
 // the time is the chain of path, table, codes, and the launches: one row in 4 layers 5 us with

@@ -380,8 +380,9 @@ class KVCache:
         """Of each row's last tokens (starts[r + 1] - starts[r] of them, or one) keeps those that
         its path names, in every layer: token number path[r, k] of them becomes number k
         (bqd_kv_accept).  path int32 [rows, width] rises and ends before the first entry that does
-        not, as ``spec_tree_verify`` returns it.  Returns the cache that takes this one's place;
-        pages that no row lists any more are free."""
+        not, as ``spec_tree_verify`` returns it.  A row with fewer tokens than nodes has a node for
+        each, counted from its first token.  Returns the cache that takes this one's place; pages
+        that no row lists any more are free."""
         if getattr(path, "dim", lambda: 0)() != 2 or path.shape[1] < 1:
             raise ValueError("path must be an int32 tensor [rows, width]")
         _dense(path, "path", torch.int32, (self.rows, path.shape[1]), self.device)

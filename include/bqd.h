@@ -433,7 +433,8 @@ int bqd_kv_attend(const bqd_kv_cache *cache, int layer, const void *q, int64_t q
  * tokens before the row's last n, j < lens[r] - n, and of those the ones whose bit is
  * set in its mask: token lens[r] - n + j where bit j % 64 of word j / 64 is set (itself
  * only where its own bit is; bits at or past n are not read, and tokens past 64 words
- * are seen by none).  A query without any key gives 0 and -infinity.
+ * are seen by none; with lens[r] < n the first n - lens[r] tokens are absent).  A query
+ * without any key gives 0 and -infinity.
  *   mask    device [tokens, words], words 1 .. BQD_TREE_MAX_WORDS (bqd_tree_mask)
  *   depth   device int32 [tokens]: with a window, query i is at position p = lens[r] - n
  *           + depth[i] (cut to [0, n)) and sees of the tokens before the last n only
@@ -487,6 +488,10 @@ int bqd_kv_fork(const bqd_kv_cache *from, const bqd_kv_cache *to, const int32_t 
  * lens[r] - n + k.  `to` gets the table, lens and refs that follow, as from
  * bqd_kv_fork: rows end behind what they keep, and pages that no row lists any more
  * are free.  Rows without nodes stay as they are.
+ * A row with fewer tokens than starts gives it nodes has n = lens[r], and nodes 0 .. n -
+ * 1 are its tokens from the first on.  (bqd_kv_attend_masked counts such a row's nodes
+ * from its end, like the positions of its queries: its tokens are there the last lens[r]
+ * nodes.)
  * A 16-token block that gets tokens takes s', the largest scale of the tokens that it
  * then holds; codes of another scale s become rnd(fp32(fp32(code * s) * fp32(1 / s'))),
  * the others keep their bits.
