@@ -28,10 +28,12 @@
 //   warp 15            bulk copies of the codes, and the scales
 //
 // Work.  A unit is (row, KV head, tile of rows); a unit's key steps are cut into equal
-// shares.  No host knows the rows' lengths: every CTA adds up the rows' steps and finds
-// the same share length, the one with the least estimated time, and its own place.
-// Shares leave O, m and l in scratch, and a second kernel, launched early, joins
-// them in order.  No atomics: the same bits every time.
+// shares.  No host knows the rows' lengths: a first kernel of one CTA adds up the rows'
+// steps, finds the share length with the least estimated time, and leaves each row's
+// place among the CTAs, where every CTA looks its own work up.  Shares leave O, m and l in
+// scratch, and a last kernel joins them in order; both followers are launched early.
+// No atomics: the same bits every time.  (The plan made by every CTA for itself took
+// time by the square of the rows: 1024 of 8 KV heads, 8 of them live, 4423 us.)
 // Bound by neither HBM nor the tensor cores, but by the waits between the roles of a step:
 // the tensor pipe is active 31% of the time, HBM read at 2.8 to 3.0 TB/s (4 x 65001
 // tokens, 8 KV heads of 128, 30 to 126 rows: 186 to 188 us; 252 rows: 286 us).  Which
@@ -62,7 +64,8 @@ constexpr int kSoftWarps = 8, kWarpsKV = 3;
 constexpr int kMmaWarp = kSoftWarps + 2 * kWarpsKV, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreadsM = (kCopyWarp + 1) * 32;
 constexpr int kStages = 2;          // fp16 tiles of K and of V
-constexpr int kMaxRows = 1024;      // rows that a CTA adds up
+constexpr int kMaxRows = 1024;      // rows that are planned for
+constexpr int kOwnRows = 16;        // rows up to which every CTA makes the plan
 constexpr int kMaxShares = 64;      // shares of a unit
 constexpr float kGrow = 15.0f;
 
@@ -94,10 +97,16 @@ struct Record {
     int first, count, step;
 };
 
+// CTAs and pieces of the rows before one; behind the last row: all CTAs, and the steps of a pair's share
+struct Place {
+    int cta, piece;
+};
+
 struct Scratch {
     float *pieces;
     Record *records;   // [rows * heads * tiles of max_new]
-    int most;          // pieces
+    Place *places;     // [rows + 1]
+    int most;          // pieces; 0: nothing is shared, and there is no plan
     int tiles;         // 128-row tiles of max_new
 };
 
@@ -196,59 +205,87 @@ struct Job {
     bool pair;
 };
 
-// Every CTA computes the same share length and finds its job in it.  In units of a step of 128 rows
-// a pair's step costs 2 and a share kFixed; S CTAs on `sms` SMs take the sum over sms and, beyond one
-// wave, about half a share more for the tail.
-constexpr float kFixed = 8.0f;
+// A row's tiles in pairs and alone, and the shares of each, of which `each` steps are a pair's and twice as
+// many a single tile's
+template <int D>
+struct Cuts {
+    int steps, pairs, ones, n2, n1;
+    __device__ __forceinline__ Cuts(int steps_, int tiles, int each) : steps(steps_)
+    {
+        if constexpr (Plan<D>::kTiles == 2) {
+            pairs = tiles / 2, ones = tiles & 1;
+            n2 = (steps + each - 1) / each, n1 = (steps + 2 * each - 1) / (2 * each);
+        } else {
+            pairs = 0, ones = tiles;
+            n2 = n1 = (steps + each - 1) / each;
+        }
+    }
+    __device__ __forceinline__ int64_t ctas(int heads) const { return heads * ((int64_t)pairs * n2 + (int64_t)ones * n1); }
+    __device__ __forceinline__ int64_t pieces(int heads) const
+    {
+        return heads * ((n2 > 1 ? 2ll * pairs * n2 : 0) + (n1 > 1 ? (int64_t)ones * n1 : 0));
+    }
+};
+
+// Steps of a row's keys, and its tiles of queries
+template <int D>
+__device__ __forceinline__ int steps_of(const AttendArgs &a, int L, const Span &span)
+{
+    return max(1, (L - first_key<D>(a, L, span) + Plan<D>::KT - 1) / Plan<D>::KT);
+}
+
+__device__ __forceinline__ int tiles_of(const AttendArgs &a, const Span &span) { return (span.n * a.group + 127) / 128; }
+
+// The share length, and the rows' places.  In units of a step of 128 rows a pair's step costs 2 and a share
+// kFixed; S CTAs on `sms` SMs take the sum over sms and, beyond one wave, about half a share more for the
+// tail.  The warps share the rows out, each lane with a candidate; sums are of whole numbers, so their order
+// is of no consequence.
+constexpr int kFixed = 8;
+
+struct Planning {
+    static constexpr int kWarps = kThreadsM / 32;
+    int64_t of_warp[3][kWarps][32];  // work, CTAs and pieces of each candidate
+    int steps[kMaxRows], tiles[kMaxRows], sums[2][kWarps], chosen;
+};
 
 template <int D>
-__device__ Job find_job(const AttendArgs &a, const Scratch &sc, int sms, int *row_steps, int *row_tiles, int *found,
-                        int *warp_sums, int *chosen)
+__device__ void plan_rows(const AttendArgs &a, const Scratch &sc, int sms, Planning &in, Place *places)
 {
     using P = Plan<D>;
+    constexpr int kWarps = Planning::kWarps;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, rows = a.L.rows, heads = a.L.heads;
-    const bool pairs = P::kTiles == 2;
-    if (rows > kMaxRows) {  // nothing is shared, and a CTA may find nothing
-        const int per = pairs ? (sc.tiles + 1) / 2 : sc.tiles, b = blockIdx.x, i = b % per;
-        Job j = {b / per / heads, b / per % heads, pairs ? 2 * i : i, 0, 1, -1, 0, false};
-        if (j.row >= rows) return Job{-1};
-        const Span span(a.starts, j.row, a.tokens, a.max_new);
-        const int tiles = (span.n * a.group + 127) / 128;
-        j.pair = pairs && j.tile + 1 < tiles;
-        if (j.tile >= tiles) j.row = -1;
-        return j;
-    }
+#pragma unroll 1
     for (int r = tid; r < rows; r += kThreadsM) {
         const Span span(a.starts, r, a.tokens, a.max_new);
-        const int L = a.L.length(r), lo = first_key<D>(a, L, span);
-        row_steps[r] = max(1, (L - lo + P::KT - 1) / P::KT);
-        row_tiles[r] = (span.n * a.group + 127) / 128;
+        in.steps[r] = steps_of<D>(a, a.L.length(r), span);
+        in.tiles[r] = tiles_of(a, span);
     }
     __syncthreads();
-    // shares of a pair's and of a single tile's steps, of which `each` are a pair's share; what a row has of both
-    auto shares2 = [&](int steps, int each) { return (steps + each - 1) / each; };
-    auto shares1 = [&](int steps, int each) { return pairs ? (steps + 2 * each - 1) / (2 * each) : shares2(steps, each); };
-    auto twos = [&](int r) { return pairs ? row_tiles[r] / 2 : 0; };
-    auto ones = [&](int r) { return pairs ? row_tiles[r] & 1 : row_tiles[r]; };
+    int longest = 1;
+#pragma unroll 1
+    for (int r = lane; r < rows; r += 32)
+        if (in.tiles[r]) longest = max(longest, in.steps[r]);
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    // lane i tries shares of longest 2^(-i / 4) steps; lane 0 splits nothing
+    int each = max(1, (int)ceilf(longest * exp2f(-0.25f * lane)));
+    each = max(max(each, 2), (longest + kMaxShares - 1) / kMaxShares);
+    if (lane == 0) each = longest;
+    int64_t work = 0, ctas = 0, pieces = 0;
+#pragma unroll 1
+    for (int r = warp; r < rows; r += kWarps) {
+        if (!in.tiles[r]) continue;
+        const Cuts<D> c(in.steps[r], in.tiles[r], each);
+        work += heads * ((int64_t)c.pairs * (2 * c.steps + c.n2 * kFixed) + (int64_t)c.ones * (c.steps + c.n1 * kFixed));
+        ctas += c.ctas(heads), pieces += c.pieces(heads);
+    }
+    in.of_warp[0][warp][lane] = work, in.of_warp[1][warp][lane] = ctas, in.of_warp[2][warp][lane] = pieces;
+    __syncthreads();
     if (warp == 0) {
-        int longest = 1;
-        for (int r = lane; r < rows; r += 32)
-            if (row_tiles[r]) longest = max(longest, row_steps[r]);
-        longest = __reduce_max_sync(0xffffffffu, longest);
-        // lane i tries shares of longest 2^(-i / 4) steps; lane 0 splits nothing
-        int each = max(1, (int)ceilf(longest * exp2f(-0.25f * lane)));
-        each = max(max(each, 2), (longest + kMaxShares - 1) / kMaxShares);
-        if (lane == 0 || sc.most == 0) each = longest;
-        float work = 0.0f;
-        int64_t ctas = 0, pieces = 0;
-        for (int r = 0; r < rows; ++r) {
-            const int s = row_steps[r], n2 = shares2(s, each), n1 = shares1(s, each), u2 = twos(r) * heads, u1 = ones(r) * heads;
-            work += (float)u2 * (2 * s + n2 * kFixed) + (float)u1 * (s + n1 * kFixed);
-            ctas += (int64_t)u2 * n2 + (int64_t)u1 * n1;
-            pieces += (n2 > 1 ? 2ll * u2 * n2 : 0) + (n1 > 1 ? (int64_t)u1 * n1 : 0);
-        }
-        const float share = (pairs ? 2 * each : each) + kFixed;
-        float cost = work / sms;
+#pragma unroll 1
+        for (int w = 1; w < min(rows, kWarps); ++w)
+            work += in.of_warp[0][w][lane], ctas += in.of_warp[1][w][lane], pieces += in.of_warp[2][w][lane];
+        const float share = (P::kTiles == 2 ? 2 * each : each) + kFixed;
+        float cost = (float)work / sms;
         if (ctas > sms) cost += 0.5f * share;
         cost = fmaxf(cost, share);
         if (pieces > sc.most) cost = 3.0e38f;
@@ -260,24 +297,17 @@ __device__ Job find_job(const AttendArgs &a, const Scratch &sc, int sms, int *ro
             const int b = __shfl_xor_sync(0xffffffffu, best, o);
             if (c < cost || (c == cost && b < best)) cost = c, best = b;
         }
-        if (lane == best) *chosen = each;
+        if (lane == best) in.chosen = each;
     }
     __syncthreads();
-    const int each = *chosen;
+    each = in.chosen;
     // CTAs and pieces of the rows before each: a thread takes consecutive rows
-    const int per = (rows + kThreadsM - 1) / kThreadsM;
-    auto of_row = [&](int r, int &ctas, int &cut) {
-        const int n2 = shares2(row_steps[r], each), n1 = shares1(row_steps[r], each), u2 = twos(r) * heads, u1 = ones(r) * heads;
-        ctas = u2 * n2 + u1 * n1;
-        cut = (n2 > 1 ? 2 * u2 * n2 : 0) + (n1 > 1 ? u1 * n1 : 0);
-    };
+    const int per = (rows + kThreadsM - 1) / kThreadsM, first = min(tid * per, rows), last = min(first + per, rows);
     int x = 0, y = 0;
-    for (int i = 0; i < per; ++i) {
-        const int r = tid * per + i;
-        if (r >= rows) break;
-        int c, q;
-        of_row(r, c, q);
-        x += c, y += q;
+#pragma unroll 1
+    for (int r = first; r < last; ++r) {
+        const Cuts<D> c(in.steps[r], in.tiles[r], each);
+        x += (int)c.ctas(heads), y += (int)c.pieces(heads);
     }
     const int mine = x, cut = y;
 #pragma unroll
@@ -285,37 +315,78 @@ __device__ Job find_job(const AttendArgs &a, const Scratch &sc, int sms, int *ro
         const int p = __shfl_up_sync(0xffffffffu, x, o), q = __shfl_up_sync(0xffffffffu, y, o);
         if (lane >= o) x += p, y += q;
     }
-    if (lane == 31) warp_sums[2 * warp] = x, warp_sums[2 * warp + 1] = y;
-    if (tid == 0) found[0] = -1;
+    if (lane == 31) in.sums[0][warp] = x, in.sums[1][warp] = y;
     __syncthreads();
-    int at = x - mine, piece = y - cut;
-    for (int w = 0; w < warp; ++w) at += warp_sums[2 * w], piece += warp_sums[2 * w + 1];
-    const int b = blockIdx.x;
-    for (int i = 0; i < per; ++i) {
-        const int r = tid * per + i;
-        if (r >= rows) break;
-        int c, q;
-        of_row(r, c, q);
-        if (b >= at && b < at + c) found[0] = r, found[1] = b - at, found[2] = piece;  // one thread of the CTA
-        at += c, piece += q;
+    Place at = {x - mine, y - cut};
+    const int busy = min(warp, (rows + 32 * per - 1) / (32 * per));  // (warps before this one that have rows)
+#pragma unroll 1
+    for (int w = 0; w < busy; ++w) at.cta += in.sums[0][w], at.piece += in.sums[1][w];
+#pragma unroll 1
+    for (int r = first; r < last; ++r) {
+        places[r] = at;
+        const Cuts<D> c(in.steps[r], in.tiles[r], each);
+        at.cta += (int)c.ctas(heads), at.piece += (int)c.pieces(heads);
     }
-    __syncthreads();
+    if (tid == kThreadsM - 1) places[rows] = Place{at.cta, each};  // (its sums are those of all rows)
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreadsM)
+masked_plan_kernel(const AttendArgs a, const Scratch sc, int sms)
+{
+    __shared__ Planning in;
+    pdl_launch_dependents();
+    plan_rows<D>(a, sc, sms, in, sc.places);
+}
+
+// What the CTA does; its row is -1 where it has nothing to do
+template <int D>
+__device__ Job find_job(const AttendArgs &a, const Scratch &sc, int sms, Planning &in, Place *near, int *found)
+{
+    using P = Plan<D>;
+    const int rows = a.L.rows, heads = a.L.heads, b = blockIdx.x;
+    const bool pairs = P::kTiles == 2;
+    if (sc.most == 0) {
+        const int per = pairs ? (sc.tiles + 1) / 2 : sc.tiles, i = b % per;
+        Job j = {b / per / heads, b / per % heads, pairs ? 2 * i : i, 0, 1, -1, 0, false};
+        if (j.row >= rows) return Job{-1};
+        const int tiles = tiles_of(a, Span(a.starts, j.row, a.tokens, a.max_new));
+        j.pair = pairs && j.tile + 1 < tiles;
+        if (j.tile >= tiles) j.row = -1;
+        return j;
+    }
+    const Place *places = sc.places;
+    if (rows <= kOwnRows) {
+        plan_rows<D>(a, sc, sms, in, near);
+        __syncthreads();
+        places = near;
+    } else {
+        pdl_wait();
+    }
+    const Place all = places[rows];
+    if (b >= all.cta) return Job{-1};
+#pragma unroll 1
+    for (int r = threadIdx.x; r < rows; r += kThreadsM) {
+        const Place p = places[r];
+        if (b >= p.cta && b < places[r + 1].cta) found[0] = r, found[1] = b - p.cta, found[2] = p.piece;
+    }
+    __syncthreads();  // (one thread of the CTA found it)
     Job j = {found[0], 0, 0, 0, 1, -1, 0, false};
-    if (j.row < 0) return j;
     // a row's pairs first, then its single tiles; tiles fastest, then heads, then shares: CTAs that read the
     // same keys run together
     int i = found[1], first = found[2];
-    const int s = row_steps[j.row], n2 = shares2(s, each), n1 = shares1(s, each), t2 = twos(j.row), t1 = ones(j.row);
-    j.pair = i < t2 * heads * n2;
+    const Span span(a.starts, j.row, a.tokens, a.max_new);
+    const Cuts<D> c(steps_of<D>(a, a.L.length(j.row), span), tiles_of(a, span), all.piece);
+    j.pair = i < c.pairs * heads * c.n2;
     if (!j.pair) {
-        i -= t2 * heads * n2;
-        if (n2 > 1) first += 2 * t2 * heads * n2;
+        i -= c.pairs * heads * c.n2;
+        if (c.n2 > 1) first += 2 * c.pairs * heads * c.n2;
     }
-    const int t = j.pair ? t2 : t1, k = i % t;
-    j.count = j.pair ? n2 : n1;
+    const int t = j.pair ? c.pairs : c.ones, k = i % t;
+    j.count = j.pair ? c.n2 : c.n1;
     j.head = i / t % heads;
     j.share = i / (t * heads);
-    j.tile = j.pair ? 2 * k : 2 * t2 + k;
+    j.tile = j.pair ? 2 * k : 2 * c.pairs + k;
     j.step = j.pair ? 2 : 1;
     if (j.count > 1) j.piece = first + (j.head * t + k) * j.count * j.step;
     return j;
@@ -332,14 +403,15 @@ attend_masked_kernel(const AttendArgs a, const Scratch sc, int sms, unsigned lon
     __shared__ uint64_t bars[56];
     __shared__ __align__(16) float2 scales[kScaleRing][P::kBlocks];  // of a step's blocks: K's scale, log2 of V's
     __shared__ float cs_of[128];
-    __shared__ int found[4], chosen, sums[2 * (kCopyWarp + 1)];
+    __shared__ Place near[kOwnRows + 1];
+    __shared__ int found[3];
     __shared__ uint32_t tmem_at;
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    // the rows' steps and tiles take a place that is filled later
-    int *row_steps = reinterpret_cast<int *>(raw);
-    const Job job = find_job<D>(a, sc, sms, row_steps, row_steps + kMaxRows, found, sums, &chosen);
+    // a plan's working place is filled with other things later
+    static_assert(sizeof(Planning) + 1024 <= P::kSmem, "");
+    const Job job = find_job<D>(a, sc, sms, *reinterpret_cast<Planning *>(raw + (base - smem_addr(raw))), near, found);
     if (job.row < 0) return;
     const int row = job.row, head = job.head;
     const Span span(a.starts, row, a.tokens, a.max_new);
@@ -981,14 +1053,20 @@ bool configure(K kern, size_t smem, bool (&done)[64])
 // Pieces that a call may leave: two waves of pairs' shares
 int most_pieces(const AttendArgs &a) { return a.L.rows > kMaxRows ? 0 : 4 * sm_count(); }
 
-int64_t tiles_of(const AttendArgs &a) { return ((int64_t)a.max_new * a.group + 127) / 128; }
+int64_t planned_tiles(const AttendArgs &a) { return ((int64_t)a.max_new * a.group + 127) / 128; }
+
+// bytes of the records of shares, at a multiple of a Place's alignment
+int64_t record_bytes(const AttendArgs &a)
+{
+    return ((int64_t)a.L.rows * a.L.heads * planned_tiles(a) * (int64_t)sizeof(Record) + 7) / 8 * 8;
+}
 
 template <int D>
 int64_t workspace_d(const AttendArgs &a)
 {
     const int64_t most = most_pieces(a);
-    return most == 0 ? 0 : most * Plan<D>::kPiece * (int64_t)sizeof(float) +
-                               (int64_t)a.L.rows * a.L.heads * tiles_of(a) * (int64_t)sizeof(Record);
+    return most == 0 ? 0 : most * Plan<D>::kPiece * (int64_t)sizeof(float) + record_bytes(a) +
+                               ((int64_t)a.L.rows + 1) * (int64_t)sizeof(Place);
 }
 
 template <int D, int FMT>
@@ -998,28 +1076,39 @@ int launch_t(const AttendArgs &a, cudaStream_t s)
     auto kern = attend_masked_kernel<D, FMT>;
     static bool done[64] = {};
     if (!configure(kern, P::kSmem, done)) return BQD_ERR_CUDA;
-    const int64_t tiles = tiles_of(a), all = (int64_t)a.L.rows * a.L.heads * tiles;
+    const int64_t tiles = planned_tiles(a), all = (int64_t)a.L.rows * a.L.heads * tiles;
     if (all > 0x20000000) return BQD_ERR_INVALID_ARG;
     // every unit once, and what shares may add
     const int64_t units = (int64_t)a.L.rows * a.L.heads * (P::kTiles == 2 ? (tiles + 1) / 2 : tiles);
-    Scratch sc = {nullptr, nullptr, 0, (int)tiles};
+    Scratch sc = {nullptr, nullptr, nullptr, 0, (int)tiles};
     if (a.work) {
         sc.most = most_pieces(a);
         sc.pieces = static_cast<float *>(a.work);
         sc.records = reinterpret_cast<Record *>(sc.pieces + (int64_t)sc.most * P::kPiece);
+        sc.places = reinterpret_cast<Place *>(reinterpret_cast<char *>(sc.records) + record_bytes(a));
     }
-    kern<<<(unsigned)(units + sc.most), kThreadsM, P::kSmem, s>>>(a, sc, sm_count(), opt_wait_ns());
-    const cudaError_t launched = cudaGetLastError();
-    if (launched != cudaSuccess || sc.most == 0) return cuda_status(launched);
+    const bool planned = sc.most > 0 && a.L.rows > kOwnRows;
+    if (planned) {
+        masked_plan_kernel<D><<<1, kThreadsM, 0, s>>>(a, sc, sm_count());
+        const int st = cuda_status(cudaGetLastError());
+        if (st != BQD_OK) return st;
+    }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)all, 128 * D / 4 / 256);
-    cfg.blockDim = dim3(256);
+    cfg.gridDim = dim3((unsigned)(units + sc.most));
+    cfg.blockDim = dim3(kThreadsM);
+    cfg.dynamicSmemBytes = P::kSmem;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
+    cfg.numAttrs = planned ? 1 : 0;  // without a plan's kernel this one waits for whatever came before
+    const int st = cuda_status(cudaLaunchKernelEx(&cfg, kern, a, sc, sm_count(), (unsigned long long)opt_wait_ns()));
+    if (st != BQD_OK || sc.most == 0) return st;
     cfg.numAttrs = 1;
+    cfg.gridDim = dim3((unsigned)all, 128 * D / 4 / 256);
+    cfg.blockDim = dim3(256);
+    cfg.dynamicSmemBytes = 0;
     return cuda_status(cudaLaunchKernelEx(&cfg, masked_join_kernel<D>, a, sc));
 }
 
