@@ -97,22 +97,35 @@ bool many_queries(const AttendArgs &a) { return (int64_t)a.max_new * a.group > (
 
 // Masked calls: the few-query kernel reads the keys once for each 16 (query, head) columns (8 with
 // head_dim 256), the kernel of 128-row tiles once for each pair of tiles, and starts later.  Times in us
-// with u the million (row, head, key) triples that the call is planned for, measured at 12 to 60 columns,
-// one to 32 rows of 700 to 65001 tokens (few / tiles at 48 columns, head_dim 128: 11 / 23 at one row of 700,
-// 88 / 70 at 8 x 8000, 306 / 188 at 4 x 65001).
+// with u the million (row, head, key) triples that the call is planned for, measured at 4 to 60 columns,
+// one to 2000 rows of 200 to 65001 tokens (few / tiles at 48 columns, head_dim 128: 11 / 23 at one row of 700,
+// 88 / 70 at 8 x 8000, 306 / 188 at 4 x 65001).  Work beyond a wave costs what starting it costs, which
+// decides for many short rows (256 of 200 tokens: 181 / 322; of 4000: 1383 / 868).  The tokens given tell how
+// many rows are live, about.  The tile kernel has a CTA for what the others could have been, the few-query
+// kernel's shares pass them over (1024 rows, 8 of them live at 4000 tokens: 57 / 150) as long as it plans any.
+// Over 660 shapes of three head sizes the choice takes 0.6% more than the better kernel, 61% at most.
 bool many_rows(const AttendArgs &a)
 {
     struct Cost {
-        double few0, few, tile0, tile, pair;
+        double few0, few, few_unit, few_idle, tile0, tile, pair, tile_unit, tile_idle;
     };
-    const Cost c = a.head_dim == 64    ? Cost{8, 32, 17, 71, 114}
-                   : a.head_dim == 128 ? Cost{10, 48, 20, 80, 127}
-                                       : Cost{9, 84, 24, 200, 400};
+    Cost c = a.head_dim == 64    ? Cost{8, 32, 0.01, 0.0014, 17, 71, 114, 0.08, 0.009}
+             : a.head_dim == 128 ? Cost{10, 48, 0.0175, 0.0014, 20, 80, 127, 0.13, 0.013}
+                                 : Cost{9, 84, 0.0175, 0.0027, 24, 200, 400, 0.13, 0.013};
+    if (a.L.rows <= kPlannedRows) c.few_idle = 0;
+    else c.tile_idle = 0.005;  // (no plan to look up)
     const int64_t columns = (int64_t)a.max_new * a.group, each = a.head_dim == 256 ? 8 : 16, tiles = (columns + 127) / 128;
     const int64_t keys = a.window > 0 ? std::min<int64_t>(a.max_len, (int64_t)a.window + a.max_new) : a.max_len;
-    const double u = 1e-6 * (double)a.L.rows * a.L.heads * (double)keys;
-    return c.few0 + c.few * u * (double)((columns + each - 1) / each) >
-           c.tile0 + u * (c.pair * (double)(tiles / 2) + c.tile * (double)(tiles % 2));
+    const int64_t rows = std::min<int64_t>(a.L.rows, ((int64_t)a.tokens + a.max_new - 1) / a.max_new);
+    const double units = (double)rows * a.L.heads, idle = (double)(a.L.rows - rows) * a.L.heads;
+    const double u = 1e-6 * units * (double)keys, sms = sm_count();
+    const double few_tiles = (double)((columns + each - 1) / each);
+    const double ctas = (double)(a.head_dim == 256 ? tiles : (tiles + 1) / 2);
+    const double few = c.few0 + c.few * u * few_tiles + c.few_unit * std::max(0.0, units * few_tiles - 2 * sms) +
+                       c.few_idle * idle * few_tiles;
+    const double tile = c.tile0 + u * (c.pair * (double)(tiles / 2) + c.tile * (double)(tiles % 2)) +
+                        c.tile_unit * std::max(0.0, units * ctas - sms) + c.tile_idle * idle * ctas;
+    return few > tile;
 }
 
 // bytes of scratch that a call is better with, or 0

@@ -63,7 +63,7 @@ namespace {
 using namespace qmvdev;
 
 constexpr int kMaxSplit = 8;      // CTAs of a cluster (16 are placed badly: 130001 tokens, 227 us against 165)
-constexpr int kMaxPlanRows = 1024; // rows that a CTA adds up
+constexpr int kMaxPlanRows = kPlannedRows; // rows that a CTA adds up
 constexpr int kMinShare = 32;     // tiles of a share at least
 constexpr int kUnitCost = 24;     // what a unit costs beside its tiles (q, the first loads, the join), in tiles:
                                   // 32 mixed sequences 81 us with 0, 58 with 8, 45 with 24, 47 with 48

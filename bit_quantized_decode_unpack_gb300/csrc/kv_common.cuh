@@ -12,6 +12,7 @@ namespace bqd {
 namespace kv {
 
 constexpr int kBlock = BQD_KV_BLOCK;  // tokens that share a scale
+constexpr int kPlannedRows = 1024;    // rows up to which attention shares keys between CTAs
 
 // One layer of a cache (pointers already at the layer).
 struct Layer {

@@ -64,7 +64,7 @@ constexpr int kSoftWarps = 8, kWarpsKV = 3;
 constexpr int kMmaWarp = kSoftWarps + 2 * kWarpsKV, kCopyWarp = kMmaWarp + 1;
 constexpr int kThreadsM = (kCopyWarp + 1) * 32;
 constexpr int kStages = 2;          // fp16 tiles of K and of V
-constexpr int kMaxRows = 1024;      // rows that are planned for
+constexpr int kMaxRows = kPlannedRows;
 constexpr int kOwnRows = 16;        // rows up to which every CTA makes the plan
 constexpr int kMaxShares = 64;      // shares of a unit
 constexpr float kGrow = 15.0f;
