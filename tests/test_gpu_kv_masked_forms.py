@@ -73,3 +73,71 @@ def test_plans_over_many_rows_of_several_tiles(rows, n, grp):
     seen, depth = od.tree_mask(_parents(rng, news), starts_of(news))
     got, _ = _compare(c, q, qd, news, "bfloat16", seen, depth=depth, tiles=True)
     np.testing.assert_array_equal(got, _run(c, q, news, seen, 1, None, 0)[0])
+
+
+def _planned(rows, seed, top):
+    """A cache of `rows` rows with a few nodes each, planned long, and its oracle's numbers."""
+    rng = np.random.default_rng(seed)
+    news = [int(n) for n in rng.integers(0, 9, rows)]
+    lens = [n + int(top * u ** 6) for n, u in zip(news, rng.random(rows))]
+    return rng, news, lens
+
+
+@pytest.mark.parametrize("rows", [12, 40])
+def test_a_captured_call_follows_lengths_and_trees(rows):
+    """The plan is made on the device: a graph is replayed over other lengths, counts and masks, on another stream."""
+    import torch
+    _, news, lens = _planned(rows, 0, 3000)
+    most = 8 * rows
+    c = random_cache(np.random.default_rng(1), [3008] * rows, heads=2, d=128, pt=64, row_pages=6000)
+    lib = to_library(c)
+    q, qd = rounded(np.random.default_rng(2).standard_normal((most, 12, 128)) * 1.5, "float16")
+    qg, starts = q.cuda(), i32([0] * (rows + 1))
+    mask = torch.zeros((most, 1), dtype=torch.int64, device="cuda")
+    out, lse = torch.empty_like(qg), torch.empty((most, 12), device="cuda")
+    assert lib.attend_workspace(12, most, 8, masked=True) > LARGE
+    lib.attend(qg, starts, mask=mask, max_new=8, out=out, lse=lse)
+    torch.cuda.synchronize()
+    graph, stream = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        lib.attend(qg, starts, mask=mask, max_new=8, out=out, lse=lse)
+    for seed in (3, 4, 5):
+        rng, news, lens = _planned(rows, seed, 3000)
+        seen, _ = od.tree_mask(_parents(rng, news), starts_of(news))
+        out.fill_(7)
+        lib.lens.copy_(i32(lens))
+        starts.copy_(i32(starts_of(news)))
+        mask[:sum(news)] = torch.from_numpy(od.mask_words(seen, 1)).cuda()
+        stream.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(stream):
+            graph.replay()
+        torch.cuda.current_stream().wait_stream(stream)
+        c["lens"] = np.array(lens)
+        want, wlse, bound, _ = od.masked_attend(c, qd[:sum(news)], starts_of(news), seen)
+        got = out.double().cpu().numpy()
+        assert np.all(np.abs(got[:sum(news)] - want) <= bound * (1 + F16_HALF) + F16_HALF * np.abs(want) + 2.0 ** -25)
+        np.testing.assert_array_equal(lse[:sum(news)].cpu().numpy() > -np.inf, wlse > -np.inf)
+        assert np.all(got[sum(news):] == 7)
+
+
+def test_planned_calls_on_two_streams_at_once():
+    """Each call has its own scratch, and with it its own plan."""
+    import torch
+    cases = []
+    for rows, seed in ((40, 6), (90, 7)):
+        rng, news, lens = _planned(rows, seed, 2000)
+        c = random_cache(rng, lens, heads=2, d=128, pt=64, row_pages=6000)
+        lib = to_library(c)
+        q = torch.from_numpy(rng.standard_normal((sum(news), 12, 128))).half().cuda()
+        seen, _ = od.tree_mask(_parents(rng, news), starts_of(news))
+        mask, starts = torch.from_numpy(od.mask_words(seen, 1)).cuda(), i32(starts_of(news))
+        assert lib.attend_workspace(12, sum(news), 8, masked=True) > LARGE
+        cases.append((lib, q, starts, mask, lib.attend(q, starts, mask=mask, max_new=8)[0], torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for lib, q, starts, mask, _, stream, got in cases:
+            with torch.cuda.stream(stream):
+                got.append(lib.attend(q, starts, mask=mask, max_new=8)[0])
+    torch.cuda.synchronize()
+    for _, _, _, _, want, _, got in cases:
+        assert all(torch.equal(want, g) for g in got)
