@@ -28,15 +28,17 @@
 //   warp 15            bulk copies of the codes, and the scales
 //
 // Work.  A unit is (row, KV head, tile of rows); a unit's key steps are cut into equal
-// shares.  No host knows the rows' lengths: a first kernel of one CTA adds up the rows'
+// shares.  No host knows the rows' lengths: a first kernel, of one CTA, adds up the rows'
 // steps, finds the share length with the least estimated time, and leaves each row's
 // place among the CTAs, where every CTA looks its own work up.  Shares leave O, m and l in
 // scratch, and a last kernel joins them in order; both followers are launched early.
-// No atomics: the same bits every time.  (The plan made by every CTA for itself took
-// time by the square of the rows: 1024 of 8 KV heads, 8 of them live, 4423 us.)
+// No atomics: the same bits every time.  Up to 16 rows every CTA makes the plan for
+// itself, which saves that launch (8 ragged trees of up to 64 nodes 124 us, 131 with it;
+// 24 rows, 4 of them live at 4000 tokens, 41 and 37).  With more it would take time by the
+// square of the rows: 1024 of 8 KV heads, 8 of them live at 500 tokens, 4423 us and 127.
 // Bound by neither HBM nor the tensor cores, but by the waits between the roles of a step:
 // the tensor pipe is active 31% of the time, HBM read at 2.8 to 3.0 TB/s (4 x 65001
-// tokens, 8 KV heads of 128, 30 to 126 rows: 186 to 188 us; 252 rows: 286 us).  Which
+// tokens, 8 KV heads of 128, 30 to 126 rows: 187 to 189 us; 252 rows: 288 us).  Which
 // wait decides is not isolated: a conversion takes 1600 to 1900 cycles of a step's 2200 to
 // 3900, yet leaving out its loads or its stores (in a copy) left the period.  The same
 // with the keys as the 128-row operand took 210 us with e4m3 codes (179 here) and 520 for

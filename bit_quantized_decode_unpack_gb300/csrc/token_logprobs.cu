@@ -3,9 +3,10 @@
 //
 //   m = max x,  l = sum 2^((x - m) c),  s = sum 2^((x - m) c) (x - m) c,  c = log2 e
 //   log p(x) = (x - m) - ln l,   entropy = ln l - ln 2 s / l
-// Every term of s has one sign and nothing large cancels.  (x - m) c is one fma, x c -
-// M with M = m c rounded, and the sums are moved to m exactly at the end.  -infinity and
-// NaN have probability 0: they are raised to a finite value whose exponential is 0.
+// A thread's sums run against a reference R at most 8 below its m, so terms of s have both
+// signs; (x - R) c is one fma, x c - M with M = R c rounded.  At the end they are moved to m,
+// s by (m - R) c l, a few roundings of at most 12 l.  -infinity and NaN have probability
+// 0: they are raised to a finite value whose exponential is 0.
 //
 // A thread keeps its own (m, l, s), in fp32, and rescales when a batch of 64 bytes
 // brings a larger value, which is rare after the first ones.  Rank counts larger
